@@ -357,6 +357,124 @@ sz_status sz_debug_encode_stalled(sz_dtype dt, const sz_codebook* h_cb, const vo
                                   void* d_ws, size_t ws_bytes,
                                   unsigned long long wait_limit_ns, cudaStream_t stream);
 
+/* ==== Serving operators around a 4-bit paged KV cache =======================
+ *
+ * What a decode step needs next to the codec: queries and keys are normalised
+ * and rotated, the new K and V rows join a paged cache, one query token per
+ * sequence attends to it, and contexts that outgrow their budget lose the
+ * tokens of least accumulated attention weight.  The codec's pages have no
+ * counterpart: the codec moves a KV cache without loss, this cache holds it
+ * at 4.5 bits per value.  The conventions at the top of this file apply: the
+ * caller owns every buffer, no call allocates, synchronises or keeps state,
+ * and every call can be captured in a CUDA graph.  Values are bfloat16; sums,
+ * softmax statistics and norms are held in fp32.
+ *
+ * Strides are in elements; the head_dim channels of a row are contiguous.
+ * 16-byte aligned rows (8-byte for append and read) take the vectorised path.
+ *
+ * The cache is a pool of pool_pages pages (16-byte aligned, page q at d_pool
+ * + q * sz_cache_page_bytes).  page_tokens is a power of two in [16, 4096],
+ * head_dim 64 or 128.  A page is [kv_heads][page_tokens / 16] cells; a cell
+ * holds 16 tokens of one kv head in 9 D 16-bit words (D = head_dim):
+ *   [K codes 4 D][V codes 4 D][K scales D/2][V scales D/2]
+ *   K code of token t, channel 32i + 8q + 4h + e:
+ *     nibble e of K word ((t * 4 + q) * D/32 + i) * 2 + h
+ *   V code of token 8b + 2q + h, channel 32i + 4g + e:
+ *     nibble e of V word (((b * 8 + g) * 4 + q) * D/32 + i) * 2 + h
+ *   scale (bfloat16) of token 2p + h, channels 32i .. 32i + 31:
+ *     scale word (p * D/32 + i) * 2 + h
+ * A channel's value is (code - 8) * scale.  The order of the words is the one
+ * the attention's matrix instructions take their operands in; a token's words
+ * are its own, so that tokens are written and moved one by one.
+ * A sequence's tokens fill slots 0, 1, ... of the pages its block table row
+ * names: slot s lies at offset s % page_tokens of page table[s / page_tokens].
+ * A flat slot number, as append and read take it, is page * page_tokens +
+ * offset.
+ * Tables beside the pool, one entry per page, kv head and offset
+ * ([pool_pages][kv_heads][page_tokens]):
+ *   d_weight (float)  accumulated attention weight
+ *   d_pos (int32)     the token's position in its sequence
+ */
+
+/* Bytes of a page: kv_heads * page_tokens * 9/8 head_dim.  Host only; 0 for
+ * sizes outside the limits above. */
+size_t sz_cache_page_bytes(size_t head_dim, size_t kv_heads, size_t page_tokens);
+
+/* RMS norm of every query and key head and the position rotation in one pass:
+ * y = x * rsqrt(mean(x^2) + eps) * w over the head_dim (64, 128 or 256)
+ * channels of a head, then for pair (a, b) number i of the first rot_dim
+ * channels (a cos - b sin, b cos + a sin) at the angle position *
+ * d_inv_freq[i], formed in double.  Pairs are channels (i, i + rot_dim / 2),
+ * or (2i, 2i + 1) when interleaved is not 0.
+ *  d_q, d_k            [tokens][heads][head_dim] by their strides; q_heads or
+ *                      kv_heads may be 0
+ *  d_q_weight,         head_dim norm weights, or NULL: that tensor is rotated
+ *  d_k_weight          without a norm
+ *  rot_dim             a multiple of 16, 0 .. head_dim; the other channels are
+ *                      normalised only
+ *  d_inv_freq          rot_dim / 2 floats
+ *  d_positions         one int32 per token
+ *  d_q_out, d_k_out    may be the inputs (with the same strides)
+ * Asynchronous. */
+sz_status sz_qk_norm_rope(const void* d_q, int64_t q_token_stride, int64_t q_head_stride, size_t q_heads,
+                          const void* d_k, int64_t k_token_stride, int64_t k_head_stride, size_t kv_heads,
+                          size_t tokens, size_t head_dim, const void* d_q_weight, const void* d_k_weight, float eps,
+                          const float* d_inv_freq, size_t rot_dim, int interleaved, const int32_t* d_positions,
+                          void* d_q_out, int64_t q_out_token_stride, int64_t q_out_head_stride, void* d_k_out,
+                          int64_t k_out_token_stride, int64_t k_out_head_stride, cudaStream_t stream);
+
+/* Quantises K and V rows into the cache.  Per 32 channels: scale =
+ * bf16(max|x| / 7) (0 below 2^-126; the NaN 0x7FC0 when the group holds an
+ * infinity or a NaN, so that the group reads as NaN), code = 8 + round(x /
+ * scale), ties to even, clamped to 1 .. 15.
+ *  d_k, d_v     [tokens][kv_heads][head_dim] by their strides
+ *  d_slots      int64 flat slot per token; -1 leaves a token out.  Another
+ *               slot outside the pool is left out too and reported as
+ *               SZ_ERR_INVALID_ARG in *d_status.  Of tokens with the same slot
+ *               one unspecified mixture is stored
+ *  d_positions  int32 per token; needed with d_pos
+ *  d_weight     nullable: the slots' weights are set to 0
+ *  d_pos        nullable: the slots' positions are set
+ * Asynchronous. */
+sz_status sz_cache_append(const void* d_k, int64_t k_token_stride, int64_t k_head_stride, const void* d_v,
+                          int64_t v_token_stride, int64_t v_head_stride, size_t tokens, const int64_t* d_slots,
+                          const int32_t* d_positions, void* d_pool, size_t pool_pages, size_t kv_heads,
+                          size_t head_dim, size_t page_tokens, float* d_weight, int32_t* d_pos, int* d_status,
+                          cudaStream_t stream);
+
+/* The values that the cache holds at d_slots, rounded to bfloat16; rows of
+ * slot -1 and of slots outside the pool (reported) are zero. */
+sz_status sz_cache_read(const void* d_pool, size_t pool_pages, size_t kv_heads, size_t head_dim, size_t page_tokens,
+                        const int64_t* d_slots, size_t tokens, void* d_k, int64_t k_token_stride,
+                        int64_t k_head_stride, void* d_v, int64_t v_token_stride, int64_t v_head_stride,
+                        int* d_status, cudaStream_t stream);
+
+/* Bytes of device workspace for sz_cache_evict.  Host only; 0 for sizes
+ * outside the limits. */
+size_t sz_cache_evict_workspace_size(size_t batch, size_t kv_heads, size_t max_tokens);
+
+/* Cuts every sequence longer than `keep` to `keep` tokens, in place.  Each kv
+ * head keeps its own: first the tokens whose position is at least d_next_pos
+ * - recent, then those of larger d_weight (NaN counts as -infinity), then
+ * those of lower slot.  The i-th slot below keep whose token goes receives
+ * the i-th surviving token from slot keep on, with its weight and position;
+ * other tokens stay where they are.  What slots from keep on hold afterwards
+ * is not cleared.  Pages must not be shared by sequences.
+ *  d_table      int32 [batch][table_width] page ids; table_width * page_tokens
+ *               < 2^31
+ *  d_next_pos   int32 per sequence: the position its next token will have
+ *  keep         1 .. 2^31 - 1
+ *  d_new_lens   int32 per sequence: min(length, keep); not d_lens.  0 for a
+ *               length outside [0, table_width * page_tokens], which is
+ *               reported as SZ_ERR_INVALID_ARG, like a page id outside the
+ *               pool (its tokens go first and are not moved)
+ *  d_ws         256-byte aligned workspace, contents irrelevant
+ * batch is at most 65,535.  Asynchronous. */
+sz_status sz_cache_evict(void* d_pool, size_t pool_pages, size_t kv_heads, size_t head_dim, size_t page_tokens,
+                         const int32_t* d_table, size_t table_width, const int32_t* d_lens, const int32_t* d_next_pos,
+                         size_t batch, size_t keep, size_t recent, float* d_weight, int32_t* d_pos,
+                         int32_t* d_new_lens, int* d_status, void* d_ws, size_t ws_bytes, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

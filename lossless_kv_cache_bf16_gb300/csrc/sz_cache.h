@@ -1,0 +1,75 @@
+// sz_cache.h -- launch parameters of the serving operators around the 4-bit
+// cache, shared by their kernels and the C ABI layer.  Not part of the public
+// interface.
+#pragma once
+
+#include <cstdint>
+
+#include <cuda_runtime.h>
+
+namespace sz {
+
+constexpr uint32_t kCellTokens = 16;  // tokens of a cell
+
+// A pool of pages of the 4-bit cache: page p, kv head h, cell j of 16 tokens
+// starts at byte ((p * heads + h) * cells of a page + j) * 18 D.
+struct CachePool {
+    uint8_t* base;
+    uint32_t pages;
+    uint32_t heads;
+    uint32_t lg_page;  // log2 of the tokens of a page
+    uint32_t dim;
+};
+
+struct NormRopeParams {
+    const uint16_t* in[2];  // q, k (bf16 bits)
+    uint16_t* out[2];
+    int64_t in_token[2], in_head[2], out_token[2], out_head[2];  // strides in elements
+    uint32_t heads[2];
+    const uint16_t* weight[2];  // nullable: no norm
+    const float* inv_freq;
+    const int32_t* positions;
+    uint32_t tokens, dim, rot;
+    int interleaved;
+    int vec;  // every row is 16-byte aligned
+    float eps;
+};
+
+// Append, and read with `rows` as the outputs.
+struct AppendParams {
+    uint16_t* rows[2];  // k, v (bf16 bits)
+    int64_t token_stride[2], head_stride[2];
+    const int64_t* slots;
+    const int32_t* positions;  // with pos
+    uint32_t tokens;
+    CachePool pool;
+    float* weight;  // nullable
+    int32_t* pos;   // nullable
+    int* status;    // nullable
+    int vec;        // rows are 8-byte aligned
+};
+
+struct EvictParams {
+    CachePool pool;
+    const int32_t* table;
+    uint32_t table_width;
+    const int32_t* lens;
+    const int32_t* next_pos;
+    uint32_t batch;
+    uint32_t keep, recent;
+    float* weight;
+    int32_t* pos;
+    int32_t* new_lens;
+    int* status;  // nullable
+    // workspace
+    uint32_t* moves;  // [batch * heads]: moves of a (sequence, head)
+    uint32_t* pairs;  // [batch * heads][2][max_moves]: target slots, source slots
+    uint32_t max_moves;
+};
+
+cudaError_t launch_norm_rope(const NormRopeParams& p, cudaStream_t s);
+cudaError_t launch_append(const AppendParams& p, cudaStream_t s);
+cudaError_t launch_cache_read(const AppendParams& p, cudaStream_t s);
+cudaError_t launch_evict(const EvictParams& p, cudaStream_t s);
+
+}  // namespace sz

@@ -50,7 +50,7 @@ def _load() -> ctypes.CDLL:
                            "`python -m lossless_kv_cache_bf16_gb300.build`")
     lib = ctypes.CDLL(path)
     vp, sz, i32, u64p = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.POINTER(ctypes.c_ulonglong)
-    cbp = ctypes.POINTER(sz_codebook)
+    cbp, i64 = ctypes.POINTER(sz_codebook), ctypes.c_int64
     sigs = {
         "sz_encoded_size": (sz, [i32, sz, sz]),
         "sz_workspace_size": (sz, [i32, sz]),
@@ -76,6 +76,13 @@ def _load() -> ctypes.CDLL:
         "sz_decode_paged": (i32, [i32, vp, sz, sz, vp, sz, sz, vp, vp, vp]),
         "sz_concat": (i32, [i32, sz, ctypes.POINTER(vp), ctypes.POINTER(sz), ctypes.POINTER(sz), vp, sz,
                             ctypes.POINTER(sz), vp, vp]),
+        "sz_cache_page_bytes": (sz, [sz, sz, sz]),
+        "sz_qk_norm_rope": (i32, [vp, i64, i64, sz, vp, i64, i64, sz, sz, sz, vp, vp, ctypes.c_float, vp, sz, i32, vp,
+                                  vp, i64, i64, vp, i64, i64, vp]),
+        "sz_cache_append": (i32, [vp, i64, i64, vp, i64, i64, sz, vp, vp, vp, sz, sz, sz, sz, vp, vp, vp, vp]),
+        "sz_cache_read": (i32, [vp, sz, sz, sz, sz, vp, sz, vp, i64, i64, vp, i64, i64, vp, vp]),
+        "sz_cache_evict_workspace_size": (sz, [sz, sz, sz]),
+        "sz_cache_evict": (i32, [vp, sz, sz, sz, sz, vp, sz, vp, vp, sz, sz, sz, vp, vp, vp, vp, vp, sz, vp]),
     }
     for name, (res, args) in sigs.items():
         fn = getattr(lib, name)
@@ -400,3 +407,152 @@ def sz_debug_encode_stalled(dt: int, cb, x: torch.Tensor, out: torch.Tensor, out
                                        out.numel() * out.element_size(), _written_ptr(out_bytes, "out_bytes"),
                                        _dev_ptr(status, "status"), _dev_ptr(ws, "ws"),
                                        ws.numel() * ws.element_size(), wait_limit_ns, _stream(stream)))
+
+
+# ---- serving operators around the 4-bit paged KV cache -------------------------
+
+def _rows(t: torch.Tensor, what: str):
+    """Shape and strides of a bf16 CUDA tensor [rows, heads, head_dim] whose
+    channels are contiguous."""
+    if t.dtype is not torch.bfloat16 or t.dim() != 3:
+        raise ValueError(f"{what} must be a bfloat16 tensor of three dimensions")
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    shape, stride = t.shape, t.stride()
+    if stride[2] != 1 and t.numel():
+        raise ValueError(f"{what} must have contiguous channels")
+    return shape, stride
+
+
+def _written_rows(t: torch.Tensor, shape, what: str):
+    """Strides of a tensor as _rows, of the given shape, that a kernel writes:
+    no two of its rows may share memory."""
+    got, stride = _rows(t, what)
+    if got != shape:
+        raise ValueError(f"{what} must have shape {tuple(shape)}, not {tuple(got)}")
+    if not t.is_contiguous():
+        reach = 0
+        for s, n in sorted(x for x in zip(stride, got) if x[1] > 1):
+            if s <= reach:
+                raise ValueError(f"{what} must not overlap itself")
+            reach += s * (n - 1)
+    return stride
+
+
+def _typed(t: torch.Tensor | None, dtype: torch.dtype, numel: int, what: str):
+    """Pointer of a contiguous CUDA tensor of `dtype` with `numel` values (None stays None)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype:
+        raise ValueError(f"{what} must be {str(dtype).removeprefix('torch.')}")
+    if t.numel() != numel:
+        raise ValueError(f"{what} must hold {numel} values, not {t.numel()}")
+    return _dev_ptr(t, what)
+
+
+_PAGE_BYTES: dict = {}  # (head_dim, kv_heads, page_tokens) -> bytes of a page
+
+
+def _cache_pages(pool: torch.Tensor, kv_heads: int, head_dim: int, page_tokens: int) -> int:
+    """Whole pages that the pool tensor (any dtype) holds."""
+    size = _PAGE_BYTES.get((head_dim, kv_heads, page_tokens))
+    if size is None:
+        if min(head_dim, kv_heads, page_tokens) < 0:
+            raise ValueError("sizes must not be negative")
+        size = int(LIB.sz_cache_page_bytes(head_dim, kv_heads, page_tokens))
+        if size and len(_PAGE_BYTES) < 1024:
+            _PAGE_BYTES[(head_dim, kv_heads, page_tokens)] = size
+    return pool.numel() * pool.element_size() // size if size else 0
+
+
+def _table(table: torch.Tensor, batch: int):
+    shape = table.shape
+    if len(shape) != 2 or shape[0] != batch:
+        raise ValueError("table must be [batch, pages of a sequence]")
+    return _typed(table, torch.int32, batch * shape[1], "table"), shape[1]
+
+
+def sz_cache_page_bytes(head_dim: int, kv_heads: int, page_tokens: int) -> int:
+    return int(LIB.sz_cache_page_bytes(head_dim, kv_heads, page_tokens))
+
+
+def sz_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor | None, k_weight: torch.Tensor | None,
+                    eps: float, inv_freq: torch.Tensor, positions: torch.Tensor, q_out: torch.Tensor,
+                    k_out: torch.Tensor, interleaved: bool = False, stream=None) -> None:
+    """Per-head RMS norm (where a weight is given) and rotation of q [tokens,
+    q heads, D] and k [tokens, kv heads, D] into q_out and k_out (which may be
+    q and k).  inv_freq: fp32, one frequency per rotated pair."""
+    q_shape, qs = _rows(q, "q")
+    tokens, q_heads, d = q_shape
+    k_shape, ks = _rows(k, "k")
+    if k_shape[0] != tokens or k_shape[2] != d:
+        raise ValueError("q and k must have the same tokens and head dimension")
+    qos, kos = _written_rows(q_out, q_shape, "q_out"), _written_rows(k_out, k_shape, "k_out")
+    qp, kp, qop, kop = q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr()
+    if (qp == qop and qs != qos) or (kp == kop and ks != kos):
+        raise ValueError("an output over its input must have the input's strides")
+    pairs = inv_freq.numel()
+    _check("sz_qk_norm_rope", LIB.sz_qk_norm_rope(
+        qp, qs[0], qs[1], q_heads, kp, ks[0], ks[1], k_shape[1], tokens, d,
+        _typed(q_weight, torch.bfloat16, d, "q_weight"), _typed(k_weight, torch.bfloat16, d, "k_weight"), eps,
+        _typed(inv_freq, torch.float32, pairs, "inv_freq"), 2 * pairs, int(interleaved),
+        _typed(positions, torch.int32, tokens, "positions"), qop, qos[0], qos[1], kop, kos[0], kos[1],
+        _stream(stream)))
+
+
+def sz_cache_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, pool: torch.Tensor, page_tokens: int,
+                    positions: torch.Tensor | None = None, weight: torch.Tensor | None = None,
+                    pos: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None) -> None:
+    """Quantises k and v [tokens, kv heads, D] into the pool at `slots` (int64,
+    page * page_tokens + offset; -1 leaves a token out).  weight (fp32) and pos
+    (int32), one entry per page, kv head and offset, are set at those slots."""
+    shape, ks = _rows(k, "k")
+    tokens, heads, d = shape
+    v_shape, vs = _rows(v, "v")
+    if v_shape != shape:
+        raise ValueError("k and v must have the same shape")
+    if pos is not None and positions is None:
+        raise ValueError("pos needs positions")
+    pages = _cache_pages(pool, heads, d, page_tokens)
+    cells = pages * heads * page_tokens
+    _check("sz_cache_append", LIB.sz_cache_append(
+        k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], tokens, _typed(slots, torch.int64, tokens, "slots"),
+        _typed(positions, torch.int32, tokens, "positions"), _dev_ptr(pool, "pool"), pages, heads, d, page_tokens,
+        _typed(weight, torch.float32, cells, "weight"), _typed(pos, torch.int32, cells, "pos"),
+        _typed(status, torch.int32, 1, "status"), _stream(stream)))
+
+
+def sz_cache_read(pool: torch.Tensor, page_tokens: int, slots: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                  status: torch.Tensor | None = None, stream=None) -> None:
+    """Reads the values at `slots` into k and v [tokens, kv heads, D] as bf16."""
+    shape = k.shape
+    ks, vs = _written_rows(k, shape, "k"), _written_rows(v, shape, "v")
+    tokens, heads, d = shape
+    _check("sz_cache_read", LIB.sz_cache_read(
+        _dev_ptr(pool, "pool"), _cache_pages(pool, heads, d, page_tokens), heads, d, page_tokens,
+        _typed(slots, torch.int64, tokens, "slots"), tokens, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1],
+        _typed(status, torch.int32, 1, "status"), _stream(stream)))
+
+
+def sz_cache_evict_workspace_size(batch: int, kv_heads: int, max_tokens: int) -> int:
+    return int(LIB.sz_cache_evict_workspace_size(batch, kv_heads, max_tokens))
+
+
+def sz_cache_evict(pool: torch.Tensor, kv_heads: int, head_dim: int, page_tokens: int, table: torch.Tensor,
+                   lens: torch.Tensor, next_pos: torch.Tensor, keep: int, recent: int, weight: torch.Tensor,
+                   pos: torch.Tensor, new_lens: torch.Tensor, ws: torch.Tensor, status: torch.Tensor | None = None,
+                   stream=None) -> None:
+    """Cuts every sequence longer than `keep` to its `keep` most wanted tokens
+    per kv head, in place; new_lens gets the lengths left."""
+    batch = lens.numel()
+    pages = _cache_pages(pool, kv_heads, head_dim, page_tokens)
+    cells = pages * kv_heads * page_tokens
+    table_ptr, width = _table(table, batch)
+    if keep < 0 or recent < 0:
+        raise ValueError("keep and recent must not be negative")
+    _check("sz_cache_evict", LIB.sz_cache_evict(
+        _dev_ptr(pool, "pool"), pages, kv_heads, head_dim, page_tokens, table_ptr, width,
+        _typed(lens, torch.int32, batch, "lens"), _typed(next_pos, torch.int32, batch, "next_pos"), batch, keep,
+        recent, _typed(weight, torch.float32, cells, "weight"), _typed(pos, torch.int32, cells, "pos"),
+        _typed(new_lens, torch.int32, batch, "new_lens"), _typed(status, torch.int32, 1, "status"),
+        _dev_ptr(ws, "ws"), ws.numel() * ws.element_size(), _stream(stream)))
