@@ -392,7 +392,7 @@ sz_status sz_debug_encode_stalled(sz_dtype dt, const sz_codebook* h_cb, const vo
  * offset.
  * Tables beside the pool, one entry per page, kv head and offset
  * ([pool_pages][kv_heads][page_tokens]):
- *   d_weight (float)  accumulated attention weight
+ *   d_weight (float)  attention weight accumulated by sz_cache_attend
  *   d_pos (int32)     the token's position in its sequence
  */
 
@@ -448,6 +448,44 @@ sz_status sz_cache_read(const void* d_pool, size_t pool_pages, size_t kv_heads, 
                         const int64_t* d_slots, size_t tokens, void* d_k, int64_t k_token_stride,
                         int64_t k_head_stride, void* d_v, int64_t v_token_stride, int64_t v_head_stride,
                         int* d_status, cudaStream_t stream);
+
+/* Bytes of device workspace for sz_cache_attend on the current device (for
+ * 152 SMs where there is none).  max_tokens = table_width * page_tokens;
+ * weights: whether d_weight will be given (4 bytes per query head and token of
+ * the table's width then).  0 for sizes outside the limits. */
+size_t sz_cache_attend_workspace_size(size_t batch, size_t q_heads, size_t kv_heads, size_t head_dim,
+                                      size_t max_tokens, int weights);
+
+/* Attention of one query token per sequence over the cache: out = softmax(
+ * scale * q K^T) V with q_heads / kv_heads (1 .. 1024) consecutive query heads
+ * per kv head.
+ *  d_q, d_out   [batch][q_heads][head_dim] by their strides, batch <= 2048;
+ *               they must not overlap
+ *  d_table      int32 [batch][table_width] page ids; table_width * page_tokens
+ *               < 2^31.  Entries past a sequence's length are not read
+ *  d_lens       int32 tokens per sequence.  An empty sequence gives zero rows
+ *               (log-sum -infinity).  A length outside [0, table_width *
+ *               page_tokens] counts as 0, the tokens of a page id outside the
+ *               pool are left out; both are reported as SZ_ERR_INVALID_ARG in
+ *               *d_status
+ *  d_lse        nullable: float [batch][q_heads], log of the sum of
+ *               exp(scale * q k), for joining with another part of the context
+ *  d_weight     nullable: each held slot's entry grows by the sum over its
+ *               query heads of the attention weight.  Additions to a page that
+ *               two sequences share come in unspecified order
+ *  d_status     nullable; SZ_OK, SZ_ERR_INVALID_ARG, or SZ_ERR_TIMEOUT when an
+ *               in-kernel copy did not land within about 1 s
+ *  d_ws         256-byte aligned workspace, contents irrelevant
+ * For the product with V a weight times its group's scale is rounded to
+ * bfloat16.  Results do not depend on the timing of blocks.  Range: query
+ * values below 2^100 and V scales below 2^26, else infinities; a weight times
+ * V below 2^-85 loses bits.  Slots past a sequence's length may hold anything,
+ * NaN included.  Asynchronous. */
+sz_status sz_cache_attend(const void* d_q, int64_t q_seq_stride, int64_t q_head_stride, size_t batch, size_t q_heads,
+                          const void* d_pool, size_t pool_pages, size_t kv_heads, size_t head_dim, size_t page_tokens,
+                          const int32_t* d_table, size_t table_width, const int32_t* d_lens, float scale, void* d_out,
+                          int64_t out_seq_stride, int64_t out_head_stride, float* d_lse, float* d_weight,
+                          int* d_status, void* d_ws, size_t ws_bytes, cudaStream_t stream);
 
 /* Bytes of device workspace for sz_cache_evict.  Host only; 0 for sizes
  * outside the limits. */

@@ -1,0 +1,737 @@
+// sz_attend.cu -- attention of one query token per sequence over the 4-bit
+// paged cache: o = sum_j p_j v_j / sum_j p_j, p_j = exp(scale q.k_j - max).
+//
+// What bounds it: each token and kv head costs 9 D / 8 bytes of cache and
+// 4 D flops per query head, so with up to 16 query heads per kv head it is a
+// stream of the cache from HBM as long as unpacking keeps up.
+//
+// Matrix instructions.  Both products use mma.sync m16n8k16 in bf16: with 8
+// or 16 query heads per item the M = 128 rows of a tcgen05 tile would be at
+// least 7/8 padding, and the legacy rate (measured: 970 instructions per SM
+// and us) is twice what the stream needs.  Codes enter the matrix unit almost
+// without conversion: a code q in the low mantissa bits of a bf16 word whose
+// other bits are zero is the (subnormal or first normal) number q * 2^-133,
+// and in the next four bits 16 q * 2^-133, so that one AND turns a word of
+// eight codes into a pair of operands.  The powers of two are undone in fp32;
+// queries are scaled to 2^120 and weights by 2^92 beforehand (exactly), which
+// keeps products normal fp32 numbers.
+//
+//   S = Q K^T   A = query heads (rows g, g + 8), B = K codes (column = token).
+//               Each group of 32 channels sums into its own accumulator,
+//               started at -8 sum(q), which takes the codes' offset of 8
+//               away; the group's scale multiplies the accumulator.
+//   O = V^T P   A = V codes less 8 (one packed add, exact; row = channel),
+//               B = weight times the group's scale, rounded to bf16 once
+//               (column = head).
+// The S accumulator's layout is the B operand's layout, so the weights never
+// leave their thread.
+//
+// Work split.  The list of (sequence, kv head, unit of 32 tokens), with
+// kItemCost more entries per (sequence, kv head) for its fixed cost, is cut
+// into equal runs, one per warp, whatever the lengths.  A warp needs nobody
+// else: it has its own ring of bulk copies, its own running maximum and sums,
+// and writes the rows of an item that it holds whole.  Pieces of an item are
+// joined once per block in shared memory, pieces over several blocks by a
+// second kernel, both in list order: results do not depend on timing.
+#include "sz_cache.cuh"
+#include "sz_params.h"
+#include "sz_pipeline.cuh"
+
+namespace sz {
+namespace {
+
+constexpr int kPartHeads = 16;  // head rows of a partial result
+constexpr float kNegInf = -__builtin_huge_valf();
+// Weights are kept times 2^92: a weight (at most 2^8, see below) times a scale
+// up to 2^26 is still finite, and a product down to 2^-85 still has all bits
+// after the factor 2^-133 of the codes.
+constexpr float kWeightShift = 92.f;
+constexpr uint32_t kItemCost = 2;
+constexpr uint32_t kMinShare = 4;  // list entries of a warp, at least
+
+template <int D, int NT>
+struct Shape {
+    static constexpr int kWarps = NT == 1 ? 12 : 8;
+    static constexpr int kThreads = 32 * kWarps;
+    static constexpr int kHeads = 8 * NT;
+    static constexpr uint32_t kUnitBytes = 2 * Cell<D>::kBytes;
+    static constexpr int kStages = (NT == 1 ? 3 : 4) * (D == 64 ? 2 : 1);
+    static constexpr int kRow = D + 4;  // floats of a head's row of a piece, padded against bank conflicts
+    static constexpr uint32_t kPieceBytes = 4 * kHeads * kRow + 8 * kHeads;
+    static constexpr uint32_t kRingBytes = kStages * kUnitBytes;  // of a warp
+    static constexpr uint32_t kPiece = kWarps * kRingBytes;
+    static constexpr uint32_t kCost = kPiece + kWarps * kPieceBytes;
+    static constexpr uint32_t kBar = kCost + 4u * kMaxBatch;
+    static constexpr uint32_t kCount = kBar + 8u * kWarps * kStages;
+    static constexpr uint32_t kBytes = kCount + 8u * kWarps * kStages;
+    static_assert(kBytes + 1024 <= 232448, "shared memory of a block");
+    static_assert(kPieceBytes <= kRingBytes, "a warp's last piece takes its ring's place");
+};
+
+// What a warp leaves for the join of its block.
+struct Left {
+    uint32_t first;       // bit 0: a piece that continues an item; bit 1: which ends it
+    uint32_t last;        // 1: a piece that starts an item and does not end it
+    uint32_t b, item;     // of the last piece
+    uint32_t rest;        // list entries of that item after this warp's
+};
+
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1, float c0, float c1, float c2, float c3) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+}
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    mma_bf16(d, a0, a1, a2, a3, b0, b1, d[0], d[1], d[2], d[3]);
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+// Codes less 8 in units of 2^-133 (low) and of 2^-129 (high nibbles).
+__device__ __forceinline__ uint32_t low_less8(uint32_t w) { return add_bf16x2(w & 0x000F000Fu, 0x80088008u); }
+__device__ __forceinline__ uint32_t high_less8(uint32_t w) { return add_bf16x2(w & 0x00F000F0u, 0x80808080u); }
+// A reference to subtract from logits: 0 where there is no maximum yet.
+__device__ __forceinline__ float or_zero(float m) { return m == kNegInf ? 0.f : m; }
+
+// N (2 or 4) consecutive words of shared memory.
+template <int N>
+__device__ __forceinline__ void lds_words(const uint8_t* p, uint32_t (&w)[N]) {
+    if constexpr (N == 4) {
+        const uint4 v = *reinterpret_cast<const uint4*>(p);
+        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    } else {
+        const uint2 v = *reinterpret_cast<const uint2*>(p);
+        w[0] = v.x, w[1] = v.y;
+    }
+}
+
+// A place in the list: sequence, item (kv head and tile of query heads) and
+// entry of the item, of which the first kItemCost stand for its fixed cost;
+// cost[b] is the number of entries of sequence b's items, 0 for an empty one.
+struct Cursor {
+    uint32_t b, item, at;
+    __device__ __forceinline__ void next_item(uint32_t items, const uint32_t* cost, uint32_t batch) {
+        at = 0;
+        if (++item == items) {
+            item = 0;
+            do {
+                b++;
+            } while (b < batch && cost[b] == 0);
+        }
+    }
+};
+
+template <int D, int NT, bool LOGITS>
+__global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attend_kernel(const AttendParams p) {
+    using Sh = Shape<D, NT>;
+    using C = Cell<D>;
+    constexpr int W = Sh::kWarps, kG = C::kGroups, kSteps = D / 16;
+    extern __shared__ __align__(128) uint8_t smem[];
+    uint32_t* s_cost = reinterpret_cast<uint32_t*>(smem + Sh::kCost);
+    __shared__ uint32_t s_sum[W];
+    __shared__ Left s_left[W];
+    const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31u, g = lane >> 2, t = lane & 3u;
+    const uint32_t items = p.pool.heads * p.tiles;
+    const uint32_t lg_page = p.pool.lg_page;
+    const uint64_t max_tokens = (uint64_t)p.table_width << lg_page;
+    const uint32_t q_heads = p.pool.heads * p.group;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Sh::kBar) + warp * Sh::kStages;
+    uint32_t* counts = reinterpret_cast<uint32_t*>(smem + Sh::kCount) + warp * Sh::kStages * 2;
+    uint8_t* ring = smem + warp * Sh::kRingBytes;
+    if (lane == 0) {
+        for (int k = 0; k < Sh::kStages; k++) mbar_init(&bars[k], 1);
+        fence_mbar_init();
+        s_left[warp] = Left{0, 0, 0, 0, 0};
+    }
+    wait_for_previous();
+
+    // List entries of every sequence's items, and each warp's share of all.
+    // A length outside [0, table width * page tokens] counts as 0.
+    uint32_t mine = 0;
+    for (uint32_t b = tid; b < p.batch; b += Sh::kThreads) {
+        const int32_t len = p.lens[b];
+        const bool ok = len >= 0 && (uint64_t)len <= max_tokens;
+        if (!ok && p.status && blockIdx.x == 0) atomicMax(p.status, kStatusInvalid);
+        const uint32_t n = ok && len ? ((uint32_t)len + kUnitTokens - 1) / kUnitTokens + kItemCost : 0u;
+        s_cost[b] = n;
+        mine += n;
+    }
+    mine = __reduce_add_sync(0xFFFFFFFFu, mine);
+    if (lane == 0) s_sum[warp] = mine;
+    __syncthreads();
+    uint64_t total = 0;
+    for (int w = 0; w < W; w++) total += s_sum[w];
+    total *= items;
+    const uint64_t workers = (uint64_t)gridDim.x * W;
+    const uint32_t share = (uint32_t)max((total + workers - 1) / workers, (uint64_t)kMinShare);
+    const uint64_t u0 = min(((uint64_t)blockIdx.x * W + warp) * share, total);
+    const uint32_t n_run = (uint32_t)(min(u0 + share, total) - u0);
+    // Rows of empty sequences are zero, with a log-sum of -infinity.
+    for (uint32_t b = blockIdx.x; b < p.batch; b += gridDim.x) {
+        if (s_cost[b]) continue;
+        for (uint32_t x = tid; x < q_heads * D; x += Sh::kThreads)
+            p.out[(int64_t)b * p.out_seq + (int64_t)(x / D) * p.out_head + x % D] = 0;
+        for (uint32_t h = tid; h < q_heads; h += Sh::kThreads)
+            if (p.lse) p.lse[(uint64_t)b * q_heads + h] = kNegInf;
+    }
+    if (tid == 0) p.meta[4 * blockIdx.x] = -1;
+
+    // ---- where this warp's run starts: the lengths, 32 at a time ----
+    Cursor cur{0, 0, 0};
+    if (n_run) {
+        uint64_t before = 0;
+        for (uint32_t b0 = 0; b0 < p.batch; b0 += 32) {
+            const uint32_t n = b0 + lane < p.batch ? s_cost[b0 + lane] : 0u;
+            uint32_t upto = n;
+#pragma unroll
+            for (int d = 1; d < 32; d *= 2) {
+                const uint32_t o = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+                if (lane >= (uint32_t)d) upto += o;
+            }
+            const uint64_t end = before + (uint64_t)upto * items;
+            const uint32_t past = __ballot_sync(0xFFFFFFFFu, end > u0);
+            if (past) {
+                const int who = __ffs(past) - 1;
+                const uint32_t nb = __shfl_sync(0xFFFFFFFFu, n, who);
+                const uint64_t at = u0 - (__shfl_sync(0xFFFFFFFFu, end, who) - (uint64_t)nb * items);
+                cur = Cursor{b0 + (uint32_t)who, (uint32_t)(at / nb), (uint32_t)(at % nb)};
+                break;
+            }
+            before = __shfl_sync(0xFFFFFFFFu, end, 31);
+        }
+    }
+
+    // ---- this warp's ring of units ----
+    Cursor nxt = cur;
+    uint32_t nxt_left = n_run;  // list entries from nxt on
+    // Moves nxt to the next entry that is a unit.
+    auto settle = [&]() {
+        while (nxt_left) {
+            if (nxt.at < kItemCost) {
+                const uint32_t skip = min(kItemCost - nxt.at, nxt_left);
+                nxt.at += skip;
+                nxt_left -= skip;
+            } else if (nxt.at >= s_cost[nxt.b]) {
+                nxt.next_item(items, s_cost, p.batch);
+            } else {
+                break;
+            }
+        }
+    };
+    // Tokens and page of this lane's cell (lanes 0 and 1) of unit nxt, fetched
+    // one unit ahead of its copies.
+    int32_t page = 0;
+    uint32_t tokens = 0;
+    uint32_t in_flight = 0;  // stages issued and not yet waited for
+    auto look_up = [&]() {
+        settle();
+        tokens = 0;
+        if (nxt_left && lane < 2) {
+            const uint32_t first = (nxt.at - kItemCost) * kUnitTokens + lane * kCellTokens;
+            const uint32_t len = (uint32_t)p.lens[nxt.b];
+            if (first < len) {
+                tokens = min(len - first, kCellTokens);
+                page = p.table[(uint64_t)nxt.b * p.table_width + (first >> lg_page)];
+            }
+        }
+    };
+    auto issue = [&](uint32_t stage) {
+        if (nxt_left) {
+            if (tokens && (uint32_t)page >= p.pool.pages) {
+                if (p.status) atomicMax(p.status, kStatusInvalid);
+                tokens = 0;
+            }
+            const uint32_t cells = __popc(__ballot_sync(0xFFFFFFFFu, lane < 2 && tokens > 0));
+            if (lane == 0) mbar_arrive_expect_tx(&bars[stage], cells * C::kBytes);
+            if (lane < 2) counts[2 * stage + lane] = tokens;
+            __syncwarp();
+            if (lane < 2 && tokens) {
+                const uint32_t off = ((nxt.at - kItemCost) * kUnitTokens + lane * kCellTokens) & ((1u << lg_page) - 1u);
+                bulk_g2s(ring + stage * Sh::kUnitBytes + lane * C::kBytes,
+                         p.pool.base + cell_offset<D>(p.pool, (uint32_t)page, nxt.item / p.tiles, off), C::kBytes,
+                         &bars[stage]);
+            }
+            in_flight++;
+            nxt.at++;
+            nxt_left--;
+            look_up();
+        }
+    };
+    look_up();
+#pragma unroll 1
+    for (int k = 0; k < Sh::kStages; k++) issue(k);
+    uint32_t stage = 0, phase = 0;
+    bool alive = true;  // false once a wait has given up: the rest is left out
+
+    for (uint32_t left = n_run; left;) {
+        const uint32_t cost = s_cost[cur.b], take = min(left, cost - cur.at);
+        const uint32_t r0 = max(cur.at, kItemCost) - kItemCost, r1 = max(cur.at + take, kItemCost) - kItemCost;
+        const uint32_t seq = cur.b, item = cur.item;
+        left -= take;
+        cur.at += take;
+        if (cur.at == cost) cur.next_item(items, s_cost, p.batch);
+        if (r0 == r1) continue;
+        const bool starts = r0 == 0, ends = r1 == cost - kItemCost;
+        const uint32_t kv_head = item / p.tiles, tile = item % p.tiles;
+        const uint32_t head0 = kv_head * p.group + tile * Sh::kHeads;
+        const uint32_t heads = min((uint32_t)Sh::kHeads, p.group - tile * Sh::kHeads);
+
+        // ---- query operands ----
+        uint32_t qa[kSteps][2 * NT];
+        float bias[kG][NT], mult[NT];
+#pragma unroll
+        for (int n = 0; n < NT; n++) {
+            const uint32_t h = g + 8 * n;
+            uint32_t x[kG][4];
+            uint32_t top = 0;
+#pragma unroll
+            for (int i = 0; i < kG; i++) {
+                const uint16_t* src = p.q + (int64_t)seq * p.q_seq + (int64_t)(head0 + h) * p.q_head + 32 * i + 8 * t;
+#pragma unroll
+                for (int j = 0; j < 4; j++) x[i][j] = 0;
+                if (h < heads) {
+                    if (p.q_vec) {
+                        const uint4 v = *reinterpret_cast<const uint4*>(src);
+                        x[i][0] = v.x, x[i][1] = v.y, x[i][2] = v.z, x[i][3] = v.w;
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 4; j++) x[i][j] = src[2 * j] | (uint32_t)src[2 * j + 1] << 16;
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 4; j++) top = max(top, max(x[i][j] & 0x7FFFu, (x[i][j] >> 16) & 0x7FFFu));
+            }
+            top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+            top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+            // Scaled by 2^(120 - up): the largest query value's exponent, or
+            // that of the smallest normal number where all are smaller,
+            // becomes 120.  Exact; the factor in two steps, since it can be
+            // above 2^127.
+            const int up = (int)max(top >> 7, 1u) - 127;
+            const float up1 = __uint_as_float((uint32_t)(min(120 - up, 120) + 127) << 23);
+            const float up2 = __uint_as_float((uint32_t)(max(-up, 0) + 127) << 23);
+            mult[n] = ldexpf(p.scale_log2, 13 + up);
+#pragma unroll
+            for (int i = 0; i < kG; i++) {
+                float v[8], sum = 0.f;
+#pragma unroll
+                for (int j = 0; j < 8; j++) {
+                    const uint32_t bits = (j & 1) ? x[i][j >> 1] & 0xFFFF0000u : x[i][j >> 1] << 16;
+                    v[j] = __uint_as_float(bits) * up1 * up2;
+                    sum += v[j];
+                }
+                sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
+                sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
+                bias[i][n] = sum * -__uint_as_float(1u << 19);  // 8 * 2^-133
+                // Operand pair e: channels (e, 4 + e) of this thread's 8; odd
+                // e meets codes times 16.
+                qa[2 * i][n] = pack_bf16(v[0], v[4]);
+                qa[2 * i][NT + n] = pack_bf16(v[1] * 0.0625f, v[5] * 0.0625f);
+                qa[2 * i + 1][n] = pack_bf16(v[2], v[6]);
+                qa[2 * i + 1][NT + n] = pack_bf16(v[3] * 0.0625f, v[7] * 0.0625f);
+            }
+        }
+
+        float o[NT][2 * kG][4];
+        float m[NT], l[NT];  // l: this thread's share of the sum of weights
+#pragma unroll
+        for (int n = 0; n < NT; n++) {
+            m[n] = kNegInf;
+            l[n] = 0.f;
+#pragma unroll
+            for (int j = 0; j < 2 * kG; j++)
+#pragma unroll
+                for (int k = 0; k < 4; k++) o[n][j][k] = 0.f;
+        }
+
+#pragma unroll 1
+        for (uint32_t unit = r0; unit < r1; unit++) {
+            if (alive) {
+                alive = __all_sync(0xFFFFFFFFu, mbar_wait(&bars[stage], phase, p.wait_limit_ns));
+                if (!alive) {
+                    // The copies still under way must land before the block
+                    // gives its shared memory back.
+                    if (lane == 0 && p.status) atomicMax(p.status, kStatusTimeout);
+                    for (uint32_t k = 0, st = stage, ph = phase; k < in_flight; k++) {
+                        mbar_wait(&bars[st], ph, p.wait_limit_ns);
+                        if (++st == (uint32_t)Sh::kStages) st = 0, ph ^= 1u;
+                    }
+                }
+            }
+            if (!alive) break;
+            const uint8_t* u = ring + stage * Sh::kUnitBytes;
+            const uint32_t n0 = counts[2 * stage], n1 = counts[2 * stage + 1];
+            const bool whole = n0 == kCellTokens && n1 == kCellTokens;
+            // S of 32 tokens: 4 tiles of 8.
+            float s[4][2 * NT];
+#pragma unroll
+            for (int nb = 0; nb < 4; nb++) {
+                const uint8_t* cell = u + (nb >> 1) * C::kBytes;
+                uint32_t kw[kG], sw[kG];
+                lds_words<kG>(cell + ((nb & 1) * 8 + g) * (D / 2) + t * (4 * kG), kw);
+                lds_words<kG>(cell + 2 * C::kKScale + ((nb & 1) * 4 + t) * (4 * kG), sw);
+#pragma unroll
+                for (int k = 0; k < 2 * NT; k++) s[nb][k] = 0.f;
+#pragma unroll
+                for (int i = 0; i < kG; i++) {
+                    float c[4];
+                    const uint32_t w = kw[i], w8 = kw[i] >> 8;
+                    mma_bf16(c, qa[2 * i][0], NT == 2 ? qa[2 * i][NT - 1] : 0u, qa[2 * i][NT],
+                             NT == 2 ? qa[2 * i][2 * NT - 1] : 0u, w & 0x000F000Fu, w & 0x00F000F0u, bias[i][0],
+                             bias[i][0], bias[i][NT - 1], bias[i][NT - 1]);
+                    mma_bf16(c, qa[2 * i + 1][0], NT == 2 ? qa[2 * i + 1][NT - 1] : 0u, qa[2 * i + 1][NT],
+                             NT == 2 ? qa[2 * i + 1][2 * NT - 1] : 0u, w8 & 0x000F000Fu, w8 & 0x00F000F0u);
+                    const float s0 = __uint_as_float(sw[i] << 16), s1 = __uint_as_float(sw[i] & 0xFFFF0000u);
+#pragma unroll
+                    for (int n = 0; n < NT; n++) {
+                        s[nb][2 * n] = fmaf(c[2 * n], s0, s[nb][2 * n]);
+                        s[nb][2 * n + 1] = fmaf(c[2 * n + 1], s1, s[nb][2 * n + 1]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int nb = 0; nb < 4; nb++)
+#pragma unroll
+                for (int k = 0; k < 2 * NT; k++) {
+                    s[nb][k] *= mult[k >> 1];
+                    if (!whole && (nb & 1) * 8 + 2 * t + (k & 1) >= (nb >> 1 ? n1 : n0)) s[nb][k] = kNegInf;
+                }
+            if (LOGITS) {
+#pragma unroll
+                for (int n = 0; n < NT; n++)
+                    if (g + 8 * n < heads) {
+                        const uint64_t tok = (uint64_t)unit * kUnitTokens;
+                        float* row = p.logits + ((uint64_t)seq * q_heads + head0 + g + 8 * n) * max_tokens + tok + 2 * t;
+#pragma unroll
+                        for (int nb = 0; nb < 4; nb++)
+                            if (nb < 2 || tok + kCellTokens < max_tokens)
+                                *reinterpret_cast<float2*>(row + 8 * nb) = make_float2(s[nb][2 * n], s[nb][2 * n + 1]);
+                    }
+            }
+            // Running maximum, moved only when a row outgrows it by 2^8:
+            // weights stay at most 2^(92 + 8).
+            float top[NT];
+            bool grow = false;
+#pragma unroll
+            for (int n = 0; n < NT; n++) {
+                top[n] = fmaxf(s[0][2 * n], s[0][2 * n + 1]);
+#pragma unroll
+                for (int nb = 1; nb < 4; nb++) top[n] = fmaxf(top[n], fmaxf(s[nb][2 * n], s[nb][2 * n + 1]));
+                top[n] = fmaxf(top[n], __shfl_xor_sync(0xFFFFFFFFu, top[n], 1));
+                top[n] = fmaxf(top[n], __shfl_xor_sync(0xFFFFFFFFu, top[n], 2));
+                grow |= top[n] > m[n] + 8.f;
+            }
+            if (__any_sync(0xFFFFFFFFu, grow)) {
+#pragma unroll
+                for (int n = 0; n < NT; n++) {
+                    const float to = top[n] > m[n] + 8.f ? top[n] : m[n];
+                    const float f = exp2_fast(m[n] - or_zero(to));
+                    m[n] = to;
+                    l[n] *= f;
+                    // Heads 2t and 2t + 1 are this thread's columns of O.
+                    const float f0 = __shfl_sync(0xFFFFFFFFu, f, 8 * t), f1 = __shfl_sync(0xFFFFFFFFu, f, 8 * t + 4);
+#pragma unroll
+                    for (int j = 0; j < 2 * kG; j++) {
+                        o[n][j][0] *= f0, o[n][j][1] *= f1;
+                        o[n][j][2] *= f0, o[n][j][3] *= f1;
+                    }
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < NT; n++) {
+                const float ref = kWeightShift - or_zero(m[n]);
+#pragma unroll
+                for (int nb = 0; nb < 4; nb++) {
+                    s[nb][2 * n] = exp2_fast(s[nb][2 * n] + ref);
+                    s[nb][2 * n + 1] = exp2_fast(s[nb][2 * n + 1] + ref);
+                    l[n] += s[nb][2 * n] + s[nb][2 * n + 1];
+                }
+            }
+            // O += V^T P, 16 tokens (one cell) at a time.
+#pragma unroll
+            for (int c2 = 0; c2 < 2; c2++) {
+                const uint8_t* cell = u + c2 * C::kBytes;
+                uint32_t w0[kG], w1[kG], v0[kG], v1[kG];
+                lds_words<kG>(cell + 2 * C::kVScale + t * (4 * kG), v0);
+                lds_words<kG>(cell + 2 * C::kVScale + (4 + t) * (4 * kG), v1);
+                lds_words<kG>(cell + 2 * C::kV + (g * 4 + t) * (4 * kG), w0);
+                lds_words<kG>(cell + 2 * C::kV + (32 + g * 4 + t) * (4 * kG), w1);
+                if (!whole) {
+                    // Scales of slots that hold nothing may be anything: zero
+                    // times infinity must not reach the sums.
+                    const uint32_t n = c2 ? n1 : n0;
+                    const uint32_t k0 = (2 * t < n ? 0xFFFFu : 0u) | (2 * t + 1 < n ? 0xFFFF0000u : 0u);
+                    const uint32_t k1 = (8 + 2 * t < n ? 0xFFFFu : 0u) | (9 + 2 * t < n ? 0xFFFF0000u : 0u);
+#pragma unroll
+                    for (int i = 0; i < kG; i++) v0[i] &= k0, v1[i] &= k1;
+                }
+#pragma unroll
+                for (int i = 0; i < kG; i++) {
+                    const uint32_t x0 = w0[i] >> 8, x1 = w1[i] >> 8;
+                    const float s0 = __uint_as_float(v0[i] << 16), s1 = __uint_as_float(v0[i] & 0xFFFF0000u);
+                    const float s2 = __uint_as_float(v1[i] << 16), s3 = __uint_as_float(v1[i] & 0xFFFF0000u);
+                    const uint32_t a0 = low_less8(w0[i]), a1 = high_less8(w0[i]), a2 = low_less8(w1[i]), a3 = high_less8(w1[i]);
+                    const uint32_t e0 = low_less8(x0), e1 = high_less8(x0), e2 = low_less8(x1), e3 = high_less8(x1);
+#pragma unroll
+                    for (int n = 0; n < NT; n++) {
+                        const uint32_t b0 = pack_bf16(s[2 * c2][2 * n] * s0, s[2 * c2][2 * n + 1] * s1);
+                        const uint32_t b1 = pack_bf16(s[2 * c2 + 1][2 * n] * s2, s[2 * c2 + 1][2 * n + 1] * s3);
+                        mma_bf16(o[n][2 * i], a0, a1, a2, a3, b0, b1);
+                        mma_bf16(o[n][2 * i + 1], e0, e1, e2, e3, b0, b1);
+                    }
+                }
+            }
+            in_flight--;
+            __syncwarp();
+            issue(stage);
+            if (++stage == (uint32_t)Sh::kStages) stage = 0, phase ^= 1u;
+        }
+
+        // ---- the item's rows, or a piece of them ----
+        // Sums of weights are in units of 2^-92, code sums times 2^-41 (odd
+        // channels 2^-37).
+        const bool first_piece = !starts;
+        float* piece = reinterpret_cast<float*>(first_piece ? smem + Sh::kPiece + warp * Sh::kPieceBytes : ring);
+        if (!starts || !ends) __syncwarp();
+#pragma unroll
+        for (int n = 0; n < NT; n++) {
+            l[n] += __shfl_xor_sync(0xFFFFFFFFu, l[n], 1);
+            l[n] += __shfl_xor_sync(0xFFFFFFFFu, l[n], 2);
+            l[n] *= 2.0194839173657902e-28f;
+#pragma unroll
+            for (int j = 0; j < 2 * kG; j++) {
+                o[n][j][0] *= 2199023255552.f, o[n][j][1] *= 2199023255552.f;
+                o[n][j][2] *= 137438953472.f, o[n][j][3] *= 137438953472.f;
+            }
+            const float l0 = __shfl_sync(0xFFFFFFFFu, l[n], 8 * t), l1 = __shfl_sync(0xFFFFFFFFu, l[n], 8 * t + 4);
+            const uint32_t h = 8 * n + 2 * t;
+            if (starts && ends) {
+                const float i0 = 1.f / l0, i1 = 1.f / l1;
+                uint16_t* dst = p.out + (int64_t)seq * p.out_seq + (int64_t)(head0 + h) * p.out_head + 4 * g;
+#pragma unroll
+                for (int i = 0; i < kG; i++) {
+                    const float(&a)[4] = o[n][2 * i];
+                    const float(&b)[4] = o[n][2 * i + 1];
+                    const uint2 r[2] = {make_uint2(pack_bf16(a[0] * i0, a[2] * i0), pack_bf16(b[0] * i0, b[2] * i0)),
+                                        make_uint2(pack_bf16(a[1] * i1, a[3] * i1), pack_bf16(b[1] * i1, b[3] * i1))};
+#pragma unroll
+                    for (int k = 0; k < 2; k++) {
+                        if (h + k >= heads) continue;
+                        uint16_t* d = dst + k * p.out_head + 32 * i;
+                        if (p.out_vec) {
+                            *reinterpret_cast<uint2*>(d) = r[k];
+                        } else {
+                            d[0] = (uint16_t)r[k].x, d[1] = (uint16_t)(r[k].x >> 16);
+                            d[2] = (uint16_t)r[k].y, d[3] = (uint16_t)(r[k].y >> 16);
+                        }
+                    }
+                }
+                if (t == 0 && g + 8 * n < heads) {
+                    const uint64_t row = (uint64_t)seq * q_heads + head0 + g + 8 * n;
+                    const float lse2 = m[n] + log2f(l[n]);
+                    if (p.lse) p.lse[row] = lse2 * 0.6931471805599453f;
+                    if (LOGITS) p.lse2[row] = lse2;
+                }
+            } else {
+                if (t == 0) {
+                    float2* ml = reinterpret_cast<float2*>(piece + Sh::kHeads * Sh::kRow);
+                    ml[g + 8 * n] = make_float2(m[n], l[n]);
+                }
+#pragma unroll
+                for (int i = 0; i < kG; i++) {
+                    const float(&a)[4] = o[n][2 * i];
+                    const float(&b)[4] = o[n][2 * i + 1];
+                    float* row = piece + h * Sh::kRow + 32 * i + 4 * g;
+                    *reinterpret_cast<float4*>(row) = make_float4(a[0], a[2], b[0], b[2]);
+                    *reinterpret_cast<float4*>(row + Sh::kRow) = make_float4(a[1], a[3], b[1], b[3]);
+                }
+            }
+        }
+        if (lane == 0) {
+            if (first_piece) {
+                s_left[warp].first = ends ? 3u : 1u;
+            } else if (!ends) {
+                s_left[warp].last = 1;
+                s_left[warp].b = seq;
+                s_left[warp].item = item;
+                s_left[warp].rest = cost - kItemCost - r1;
+            }
+        }
+    }
+
+    // ---- join the pieces of items that several warps of this block hold ----
+    __syncthreads();
+    auto first_of = [&](int w) { return reinterpret_cast<const float*>(smem + Sh::kPiece + w * Sh::kPieceBytes); };
+    for (int w0 = -1; w0 < W; w0++) {
+        // w0 = -1: the item that the block before this one left; else the one
+        // that warp w0 started.
+        if (w0 < 0 ? !(s_left[0].first & 1u) : !s_left[w0].last) continue;
+        int w1 = w0 + 1;  // one past the last warp with a piece
+        bool ends = false;
+        while (w1 < W && !ends) ends = (s_left[w1++].first & 2u) != 0;
+        const uint32_t seq = w0 < 0 ? 0u : s_left[w0].b, item = w0 < 0 ? 0u : s_left[w0].item;
+        const uint32_t kv_head = item / p.tiles, tile = item % p.tiles;
+        const uint32_t head0 = kv_head * p.group + tile * Sh::kHeads;
+        const uint32_t heads = w0 < 0 ? (uint32_t)Sh::kHeads : min((uint32_t)Sh::kHeads, p.group - tile * Sh::kHeads);
+        auto piece_of = [&](int w) { return w == w0 ? reinterpret_cast<const float*>(smem + w * Sh::kRingBytes) : first_of(w); };
+        const uint32_t slot = 2 * blockIdx.x + (w0 < 0 ? 0u : 1u);
+        for (uint32_t x = tid; x < heads * (D / 4); x += Sh::kThreads) {
+            const uint32_t h = x / (D / 4), c = 4 * (x % (D / 4));
+            float top = kNegInf;
+            for (int w = max(w0, 0); w < w1; w++)
+                top = fmaxf(top, reinterpret_cast<const float2*>(piece_of(w) + Sh::kHeads * Sh::kRow)[h].x);
+            const float ref = or_zero(top);
+            float l = 0.f, a[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int w = max(w0, 0); w < w1; w++) {
+                const float* piece = piece_of(w);
+                const float2 ml = reinterpret_cast<const float2*>(piece + Sh::kHeads * Sh::kRow)[h];
+                const float4 v = *reinterpret_cast<const float4*>(piece + h * Sh::kRow + c);
+                const float f = exp2_fast(ml.x - ref);
+                l = fmaf(f, ml.y, l);
+                a[0] = fmaf(f, v.x, a[0]), a[1] = fmaf(f, v.y, a[1]), a[2] = fmaf(f, v.z, a[2]), a[3] = fmaf(f, v.w, a[3]);
+            }
+            if (w0 >= 0 && ends) {
+                const float inv = 1.f / l;
+                uint16_t* dst = p.out + (int64_t)seq * p.out_seq + (int64_t)(head0 + h) * p.out_head + c;
+#pragma unroll
+                for (int k = 0; k < 4; k++) dst[k] = (uint16_t)bf16_bits(a[k] * inv);
+                if (c == 0) {
+                    const uint64_t row = (uint64_t)seq * q_heads + head0 + h;
+                    const float lse2 = top + log2f(l);
+                    if (p.lse) p.lse[row] = lse2 * 0.6931471805599453f;
+                    if (LOGITS) p.lse2[row] = lse2;
+                }
+            } else {
+                if (c == 0) *reinterpret_cast<float2*>(p.part_ml + (slot * kPartHeads + h) * 2) = make_float2(top, l);
+                *reinterpret_cast<float4*>(p.part_o + ((uint64_t)slot * kPartHeads + h) * D + c) =
+                    make_float4(a[0], a[1], a[2], a[3]);
+            }
+        }
+        if (w0 >= 0 && !ends && tid == 0) {
+            // The blocks after this one that hold the rest of the item.
+            const uint64_t here = (uint64_t)(W - 1 - w0) * share, run = (uint64_t)W * share;
+            p.meta[4 * blockIdx.x + 1] = (int32_t)item;
+            p.meta[4 * blockIdx.x + 2] = (int32_t)((s_left[w0].rest - here + run - 1) / run);
+            p.meta[4 * blockIdx.x] = (int32_t)seq;
+        }
+    }
+}
+
+// Joins the partial sums of the item that block blockIdx.x of the first
+// kernel started and did not end: its own, then those of the next blocks.
+template <int D>
+__global__ void __launch_bounds__(256) attend_join_kernel(const AttendParams p, const uint32_t item_heads) {
+    wait_for_previous();
+    const int32_t b = p.meta[4 * blockIdx.x];
+    if (b < 0) return;
+    const uint32_t item = (uint32_t)p.meta[4 * blockIdx.x + 1];
+    const int more = p.meta[4 * blockIdx.x + 2];
+    const uint32_t kv_head = item / p.tiles, tile = item % p.tiles;
+    const uint32_t head0 = kv_head * p.group + tile * item_heads;
+    const uint32_t heads = min(item_heads, p.group - tile * item_heads);
+    const uint32_t q_heads = p.pool.heads * p.group;
+    for (uint32_t x = threadIdx.x; x < heads * (D / 4); x += 256) {
+        const uint32_t h = x / (D / 4), c = 4 * (x % (D / 4));
+        auto slot = [&](int k) { return (uint64_t)(k == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + k)) * kPartHeads + h; };
+        float top = kNegInf;
+#pragma unroll 4
+        for (int k = 0; k <= more; k++) top = fmaxf(top, p.part_ml[2 * slot(k)]);
+        const float ref = or_zero(top);
+        float l = 0.f, a[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+        for (int k = 0; k <= more; k++) {
+            const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * slot(k));
+            const float4 v = *reinterpret_cast<const float4*>(p.part_o + slot(k) * D + c);
+            const float f = exp2_fast(ml.x - ref);
+            l = fmaf(f, ml.y, l);
+            a[0] = fmaf(f, v.x, a[0]), a[1] = fmaf(f, v.y, a[1]), a[2] = fmaf(f, v.z, a[2]), a[3] = fmaf(f, v.w, a[3]);
+        }
+        const float inv = 1.f / l;
+        uint16_t* dst = p.out + (int64_t)b * p.out_seq + (int64_t)(head0 + h) * p.out_head + c;
+#pragma unroll
+        for (int k = 0; k < 4; k++) dst[k] = (uint16_t)bf16_bits(a[k] * inv);
+        if (c == 0) {
+            const uint64_t row = (uint64_t)b * q_heads + head0 + h;
+            const float lse2 = top + log2f(l);
+            if (p.lse) p.lse[row] = lse2 * 0.6931471805599453f;
+            if (p.weight) p.lse2[row] = lse2;
+        }
+    }
+}
+
+// weight[slot] += sum over the kv head's query heads of the step's attention
+// weight, from the logits that the first kernel kept.  A slot gets one
+// addition per call and sequence; atomic, for pages that two sequences share.
+__global__ void __launch_bounds__(256) attend_weight_kernel(const AttendParams p) {
+    wait_for_previous();
+    const uint32_t b = blockIdx.z, kv_head = blockIdx.y;
+    const int32_t len = p.lens[b];
+    const uint64_t max_tokens = (uint64_t)p.table_width << p.pool.lg_page;
+    if (len <= 0 || (uint64_t)len > max_tokens) return;
+    const uint32_t q_heads = p.pool.heads * p.group;
+    const uint64_t row0 = (uint64_t)b * q_heads + (uint64_t)kv_head * p.group;
+    for (uint32_t tok = (blockIdx.x * 256 + threadIdx.x) * 2; tok < (uint32_t)len; tok += gridDim.x * 512) {
+        const int32_t page = p.table[(uint64_t)b * p.table_width + (tok >> p.pool.lg_page)];
+        if ((uint32_t)page >= p.pool.pages) continue;
+        float w0 = 0.f, w1 = 0.f;
+#pragma unroll 4
+        for (uint32_t h = 0; h < p.group; h++) {
+            const float2 s = *reinterpret_cast<const float2*>(p.logits + (row0 + h) * max_tokens + tok);
+            const float lse2 = p.lse2[row0 + h];
+            w0 += exp2_fast(s.x - lse2);
+            w1 += exp2_fast(s.y - lse2);
+        }
+        float* dst = p.weight + ((((uint64_t)(uint32_t)page * p.pool.heads + kv_head) << p.pool.lg_page) +
+                                 (tok & ((1u << p.pool.lg_page) - 1u)));
+        atomicAdd(dst, w0);
+        if (tok + 1 < (uint32_t)len) atomicAdd(dst + 1, w1);
+    }
+}
+
+template <int D, int NT, bool LOGITS>
+cudaError_t launch(const AttendParams& p, cudaStream_t s) {
+    using Sh = Shape<D, NT>;
+    int sms = 0, per_sm = 0;
+    cudaError_t err = kernel_fit(reinterpret_cast<const void*>(attend_kernel<D, NT, LOGITS>), Sh::kThreads, Sh::kBytes, &sms, &per_sm);
+    if (err != cudaSuccess) return err;
+    err = launch_dependent(attend_kernel<D, NT, LOGITS>, dim3((uint32_t)sms), dim3(Sh::kThreads), Sh::kBytes, s, p);
+    if (err != cudaSuccess) return err;
+    err = launch_dependent(attend_join_kernel<D>, dim3((uint32_t)sms), dim3(256), 0, s, p, (uint32_t)Sh::kHeads);
+    if (err != cudaSuccess || !LOGITS) return err;
+    const uint64_t tokens = (uint64_t)p.table_width << p.pool.lg_page;
+    const uint32_t blocks = (uint32_t)((tokens + 511) / 512);
+    return launch_dependent(attend_weight_kernel, dim3(blocks < 1024 ? blocks : 1024, p.pool.heads, p.batch), dim3(256), 0, s, p);
+}
+
+template <int D>
+cudaError_t launch_dim(const AttendParams& p, cudaStream_t s) {
+    if (p.group <= 8) return p.weight ? launch<D, 1, true>(p, s) : launch<D, 1, false>(p, s);
+    return p.weight ? launch<D, 2, true>(p, s) : launch<D, 2, false>(p, s);
+}
+
+}  // namespace
+
+cudaError_t attend_shape(uint32_t group, uint32_t* item_heads, uint32_t* blocks) {
+    *item_heads = group <= 8 ? 8 : 16;
+    int dev = -1, sms = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err == cudaSuccess) err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    *blocks = (uint32_t)sms;
+    return err;
+}
+
+cudaError_t launch_attend(const AttendParams& p, cudaStream_t s) {
+    return p.pool.dim == 64 ? launch_dim<64>(p, s) : launch_dim<128>(p, s);
+}
+
+}  // namespace sz

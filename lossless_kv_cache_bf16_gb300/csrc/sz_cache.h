@@ -10,6 +10,8 @@
 namespace sz {
 
 constexpr uint32_t kCellTokens = 16;  // tokens of a cell
+constexpr uint32_t kUnitTokens = 32;  // tokens that a warp of the attention takes at a time (two cells)
+constexpr uint32_t kMaxBatch = 2048;  // sequences of one attention call (their lengths sit in shared memory)
 
 // A pool of pages of the 4-bit cache: page p, kv head h, cell j of 16 tokens
 // starts at byte ((p * heads + h) * cells of a page + j) * 18 D.
@@ -49,6 +51,32 @@ struct AppendParams {
     int vec;        // rows are 8-byte aligned
 };
 
+struct AttendParams {
+    const uint16_t* q;
+    int64_t q_seq, q_head;
+    uint16_t* out;
+    int64_t out_seq, out_head;
+    CachePool pool;
+    const int32_t* table;
+    uint32_t table_width;
+    const int32_t* lens;
+    uint32_t batch;
+    uint32_t group;    // query heads per kv head
+    uint32_t tiles;    // work items per kv head: ceil(group / heads of an item)
+    float scale_log2;  // softmax scale * log2(e)
+    float* lse;        // nullable [batch][q heads]
+    float* weight;     // nullable
+    int* status;       // nullable
+    uint64_t wait_limit_ns;
+    int q_vec, out_vec;  // query rows are 16-byte, output rows 8-byte aligned
+    // workspace
+    int32_t* meta;   // [blocks][4]
+    float* part_ml;  // [blocks][2][16][2]: maximum, sum of weights
+    float* part_o;   // [blocks][2][16][dim]
+    float* lse2;     // [batch][q heads], log2; with weight
+    float* logits;   // [batch][q heads][max tokens], log2; with weight
+};
+
 struct EvictParams {
     CachePool pool;
     const int32_t* table;
@@ -70,6 +98,9 @@ struct EvictParams {
 cudaError_t launch_norm_rope(const NormRopeParams& p, cudaStream_t s);
 cudaError_t launch_append(const AppendParams& p, cudaStream_t s);
 cudaError_t launch_cache_read(const AppendParams& p, cudaStream_t s);
+// Query heads of one attention work item, and blocks of its launch on this device.
+cudaError_t attend_shape(uint32_t group, uint32_t* item_heads, uint32_t* blocks);
+cudaError_t launch_attend(const AttendParams& p, cudaStream_t s);
 cudaError_t launch_evict(const EvictParams& p, cudaStream_t s);
 
 }  // namespace sz

@@ -81,6 +81,9 @@ def _load() -> ctypes.CDLL:
                                   vp, i64, i64, vp, i64, i64, vp]),
         "sz_cache_append": (i32, [vp, i64, i64, vp, i64, i64, sz, vp, vp, vp, sz, sz, sz, sz, vp, vp, vp, vp]),
         "sz_cache_read": (i32, [vp, sz, sz, sz, sz, vp, sz, vp, i64, i64, vp, i64, i64, vp, vp]),
+        "sz_cache_attend_workspace_size": (sz, [sz, sz, sz, sz, sz, i32]),
+        "sz_cache_attend": (i32, [vp, i64, i64, sz, sz, vp, sz, sz, sz, sz, vp, sz, vp, ctypes.c_float, vp, i64, i64,
+                                  vp, vp, vp, vp, sz, vp]),
         "sz_cache_evict_workspace_size": (sz, [sz, sz, sz]),
         "sz_cache_evict": (i32, [vp, sz, sz, sz, sz, vp, sz, vp, vp, sz, sz, sz, vp, vp, vp, vp, vp, sz, vp]),
     }
@@ -532,6 +535,36 @@ def sz_cache_read(pool: torch.Tensor, page_tokens: int, slots: torch.Tensor, k: 
         _dev_ptr(pool, "pool"), _cache_pages(pool, heads, d, page_tokens), heads, d, page_tokens,
         _typed(slots, torch.int64, tokens, "slots"), tokens, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1],
         _typed(status, torch.int32, 1, "status"), _stream(stream)))
+
+
+def sz_cache_attend_workspace_size(batch: int, q_heads: int, kv_heads: int, head_dim: int, max_tokens: int,
+                                   weights: bool = False) -> int:
+    return int(LIB.sz_cache_attend_workspace_size(batch, q_heads, kv_heads, head_dim, max_tokens, int(weights)))
+
+
+def sz_cache_attend(q: torch.Tensor, pool: torch.Tensor, kv_heads: int, page_tokens: int, table: torch.Tensor,
+                    lens: torch.Tensor, scale: float, out: torch.Tensor, ws: torch.Tensor,
+                    lse: torch.Tensor | None = None, weight: torch.Tensor | None = None,
+                    status: torch.Tensor | None = None, stream=None) -> None:
+    """Attention of q [batch, q heads, D], one token per sequence, over the
+    cache: sequence b's lens[b] tokens lie in the pages table[b].  lse (fp32
+    [batch, q heads]) gets the log-sums; weight (fp32, one entry per page, kv
+    head and offset) grows by the attention weights."""
+    shape, qs = _rows(q, "q")
+    batch, q_heads, d = shape
+    os = _written_rows(out, shape, "out")
+    qp, op = q.data_ptr(), out.data_ptr()
+    if qp == op and batch:
+        raise ValueError("out must not be q")
+    pages = _cache_pages(pool, kv_heads, d, page_tokens)
+    table_ptr, width = _table(table, batch)
+    _check("sz_cache_attend", LIB.sz_cache_attend(
+        qp, qs[0], qs[1], batch, q_heads, _dev_ptr(pool, "pool"), pages, kv_heads, d, page_tokens, table_ptr, width,
+        _typed(lens, torch.int32, batch, "lens"), scale, op, os[0], os[1],
+        _typed(lse, torch.float32, batch * q_heads, "lse"),
+        _typed(weight, torch.float32, pages * kv_heads * page_tokens, "weight"),
+        _typed(status, torch.int32, 1, "status"), _dev_ptr(ws, "ws"), ws.numel() * ws.element_size(),
+        _stream(stream)))
 
 
 def sz_cache_evict_workspace_size(batch: int, kv_heads: int, max_tokens: int) -> int:

@@ -127,7 +127,8 @@ def norm_rope(x, w, eps, inv_freq, positions, interleaved):
 
 def attend(q, k, v, scale):
     """One sequence: q [Hq, D], k, v float64 [n, H, D].  Returns (out, sum of
-    weight * |v|, lse, weights [H, n], largest sum |q k scale|)."""
+    weight * |v|, lse, weights [H, n], largest sum of what a kernel adds up for
+    a logit: |scale q| (|code - 8| + 8) s, with 7 s the largest |k| of a group)."""
     hq, d = q.shape
     n, h, _ = k.shape
     if n == 0:
@@ -139,7 +140,8 @@ def attend(q, k, v, scale):
     p = torch.exp(s - lse[..., None])
     out = torch.einsum("hgn,nhd->hgd", p, v)
     mag = torch.einsum("hgn,nhd->hgd", p, v.abs())
-    reach = float((torch.einsum("hgd,nhd->hgn", qg.abs(), k.abs()) * abs(scale)).max())
+    kk = (k.abs().unflatten(-1, (-1, 32)) + 8 / 7 * k.abs().unflatten(-1, (-1, 32)).amax(-1, keepdim=True)).flatten(-2)
+    reach = float((torch.einsum("hgd,nhd->hgn", qg.abs(), kk) * abs(scale)).max())
     return out.reshape(hq, d), mag.reshape(hq, d), lse.reshape(hq), p.sum(1), reach
 
 
