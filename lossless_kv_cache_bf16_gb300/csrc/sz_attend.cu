@@ -17,9 +17,9 @@
 // keeps products normal fp32 numbers.
 //
 //   S = Q K^T   A = query heads (rows g, g + 8), B = K codes (column = token).
-//               Each group of 32 channels sums into its own accumulator,
-//               started at -8 sum(q), which takes the codes' offset of 8
-//               away; the group's scale multiplies the accumulator.
+//               Each group of 32 channels sums into its own accumulator;
+//               -8 sum(q) takes the codes' offset of 8 away, and the group's
+//               scale multiplies the rest.
 //   O = V^T P   A = V codes less 8 (one packed add, exact; row = channel),
 //               B = weight times the group's scale, rounded to bf16 once
 //               (column = head).
@@ -51,11 +51,11 @@ constexpr uint32_t kMinShare = 4;  // list entries of a warp, at least
 
 template <int D, int NT>
 struct Shape {
-    static constexpr int kWarps = NT == 1 ? 12 : 8;
+    static constexpr int kWarps = NT == 1 ? 16 : 8;
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kHeads = 8 * NT;
     static constexpr uint32_t kUnitBytes = 2 * Cell<D>::kBytes;
-    static constexpr int kStages = (NT == 1 ? 3 : 4) * (D == 64 ? 2 : 1);
+    static constexpr int kStages = (NT == 1 ? 2 : 4) * (D == 64 ? 2 : 1);
     static constexpr int kRow = D + 4;  // floats of a head's row of a piece, padded against bank conflicts
     static constexpr uint32_t kPieceBytes = 4 * kHeads * kRow + 8 * kHeads;
     static constexpr uint32_t kRingBytes = kStages * kUnitBytes;  // of a warp
@@ -77,16 +77,40 @@ struct Left {
 };
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1, float c0, float c1, float c2, float c3) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
-        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
-}
-__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
-    mma_bf16(d, a0, a1, a2, a3, b0, b1, d[0], d[1], d[2], d[3]);
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// The same into a fresh accumulator.
+__device__ __forceinline__ void mma_bf16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+// Pairs of floats in one register pair: one instruction for two sums.
+struct F2 {
+    uint64_t v;
+    __device__ __forceinline__ F2(float x, float y) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y)); }
+    __device__ __forceinline__ void get(float& x, float& y) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v)); }
+};
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(a.v) : "l"(a.v), "l"(b.v));
+    return a;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(a.v) : "l"(a.v), "l"(b.v));
+    return a;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(a.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return a;
+}
+// Two packed bf16 as floats.
+__device__ __forceinline__ F2 unpack_bf16(uint32_t w) { return F2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)); }
 __device__ __forceinline__ float exp2_fast(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -316,11 +340,12 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attend_kernel(const
             // Scaled by 2^(120 - up): the largest query value's exponent, or
             // that of the smallest normal number where all are smaller,
             // becomes 120.  Exact; the factor in two steps, since it can be
-            // above 2^127.
+            // above 2^127.  The softmax scale's sign goes with the queries, so
+            // that the largest sum is the largest logit.
             const int up = (int)max(top >> 7, 1u) - 127;
-            const float up1 = __uint_as_float((uint32_t)(min(120 - up, 120) + 127) << 23);
+            const float up1 = copysignf(__uint_as_float((uint32_t)(min(120 - up, 120) + 127) << 23), p.scale_log2);
             const float up2 = __uint_as_float((uint32_t)(max(-up, 0) + 127) << 23);
-            mult[n] = ldexpf(p.scale_log2, 13 + up);
+            mult[n] = ldexpf(fabsf(p.scale_log2), 13 + up);
 #pragma unroll
             for (int i = 0; i < kG; i++) {
                 float v[8], sum = 0.f;
@@ -380,32 +405,30 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attend_kernel(const
                 uint32_t kw[kG], sw[kG];
                 lds_words<kG>(cell + ((nb & 1) * 8 + g) * (D / 2) + t * (4 * kG), kw);
                 lds_words<kG>(cell + 2 * C::kKScale + ((nb & 1) * 4 + t) * (4 * kG), sw);
-#pragma unroll
-                for (int k = 0; k < 2 * NT; k++) s[nb][k] = 0.f;
+                F2 sum[2] = {F2(0.f, 0.f), F2(0.f, 0.f)};
 #pragma unroll
                 for (int i = 0; i < kG; i++) {
                     float c[4];
                     const uint32_t w = kw[i], w8 = kw[i] >> 8;
-                    mma_bf16(c, qa[2 * i][0], NT == 2 ? qa[2 * i][NT - 1] : 0u, qa[2 * i][NT],
-                             NT == 2 ? qa[2 * i][2 * NT - 1] : 0u, w & 0x000F000Fu, w & 0x00F000F0u, bias[i][0],
-                             bias[i][0], bias[i][NT - 1], bias[i][NT - 1]);
+                    mma_bf16_first(c, qa[2 * i][0], NT == 2 ? qa[2 * i][NT - 1] : 0u, qa[2 * i][NT],
+                                   NT == 2 ? qa[2 * i][2 * NT - 1] : 0u, w & 0x000F000Fu, w & 0x00F000F0u);
                     mma_bf16(c, qa[2 * i + 1][0], NT == 2 ? qa[2 * i + 1][NT - 1] : 0u, qa[2 * i + 1][NT],
                              NT == 2 ? qa[2 * i + 1][2 * NT - 1] : 0u, w8 & 0x000F000Fu, w8 & 0x00F000F0u);
-                    const float s0 = __uint_as_float(sw[i] << 16), s1 = __uint_as_float(sw[i] & 0xFFFF0000u);
+                    const F2 scale = unpack_bf16(sw[i]);
 #pragma unroll
-                    for (int n = 0; n < NT; n++) {
-                        s[nb][2 * n] = fmaf(c[2 * n], s0, s[nb][2 * n]);
-                        s[nb][2 * n + 1] = fmaf(c[2 * n + 1], s1, s[nb][2 * n + 1]);
-                    }
+                    for (int n = 0; n < NT; n++)
+                        sum[n] = fma2(add2(F2(c[2 * n], c[2 * n + 1]), F2(bias[i][n], bias[i][n])), scale, sum[n]);
                 }
+#pragma unroll
+                for (int n = 0; n < NT; n++) sum[n].get(s[nb][2 * n], s[nb][2 * n + 1]);
             }
+            if (!whole) {
 #pragma unroll
-            for (int nb = 0; nb < 4; nb++)
+                for (int nb = 0; nb < 4; nb++)
 #pragma unroll
-                for (int k = 0; k < 2 * NT; k++) {
-                    s[nb][k] *= mult[k >> 1];
-                    if (!whole && (nb & 1) * 8 + 2 * t + (k & 1) >= (nb >> 1 ? n1 : n0)) s[nb][k] = kNegInf;
-                }
+                    for (int k = 0; k < 2 * NT; k++)
+                        if ((nb & 1) * 8 + 2 * t + (k & 1) >= (nb >> 1 ? n1 : n0)) s[nb][k] = kNegInf;
+            }
             if (LOGITS) {
 #pragma unroll
                 for (int n = 0; n < NT; n++)
@@ -415,7 +438,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attend_kernel(const
 #pragma unroll
                         for (int nb = 0; nb < 4; nb++)
                             if (nb < 2 || tok + kCellTokens < max_tokens)
-                                *reinterpret_cast<float2*>(row + 8 * nb) = make_float2(s[nb][2 * n], s[nb][2 * n + 1]);
+                                *reinterpret_cast<float2*>(row + 8 * nb) = make_float2(s[nb][2 * n] * mult[n], s[nb][2 * n + 1] * mult[n]);
                     }
             }
             // Running maximum, moved only when a row outgrows it by 2^8:
@@ -429,6 +452,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attend_kernel(const
                 for (int nb = 1; nb < 4; nb++) top[n] = fmaxf(top[n], fmaxf(s[nb][2 * n], s[nb][2 * n + 1]));
                 top[n] = fmaxf(top[n], __shfl_xor_sync(0xFFFFFFFFu, top[n], 1));
                 top[n] = fmaxf(top[n], __shfl_xor_sync(0xFFFFFFFFu, top[n], 2));
+                top[n] = top[n] == kNegInf ? kNegInf : top[n] * mult[n];
                 grow |= top[n] > m[n] + 8.f;
             }
             if (__any_sync(0xFFFFFFFFu, grow)) {
@@ -452,8 +476,13 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attend_kernel(const
                 const float ref = kWeightShift - or_zero(m[n]);
 #pragma unroll
                 for (int nb = 0; nb < 4; nb++) {
-                    s[nb][2 * n] = exp2_fast(s[nb][2 * n] + ref);
-                    s[nb][2 * n + 1] = exp2_fast(s[nb][2 * n + 1] + ref);
+                    s[nb][2 * n] = exp2_fast(fmaf(s[nb][2 * n], mult[n], ref));
+                    s[nb][2 * n + 1] = exp2_fast(fmaf(s[nb][2 * n + 1], mult[n], ref));
+                    if (!whole) {  // minus infinity times a factor of 0 is no number
+                        const uint32_t held = nb >> 1 ? n1 : n0, at = (nb & 1) * 8 + 2 * t;
+                        if (at >= held) s[nb][2 * n] = 0.f;
+                        if (at + 1 >= held) s[nb][2 * n + 1] = 0.f;
+                    }
                     l[n] += s[nb][2 * n] + s[nb][2 * n + 1];
                 }
             }
@@ -478,14 +507,15 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attend_kernel(const
 #pragma unroll
                 for (int i = 0; i < kG; i++) {
                     const uint32_t x0 = w0[i] >> 8, x1 = w1[i] >> 8;
-                    const float s0 = __uint_as_float(v0[i] << 16), s1 = __uint_as_float(v0[i] & 0xFFFF0000u);
-                    const float s2 = __uint_as_float(v1[i] << 16), s3 = __uint_as_float(v1[i] & 0xFFFF0000u);
+                    const F2 s0 = unpack_bf16(v0[i]), s1 = unpack_bf16(v1[i]);
                     const uint32_t a0 = low_less8(w0[i]), a1 = high_less8(w0[i]), a2 = low_less8(w1[i]), a3 = high_less8(w1[i]);
                     const uint32_t e0 = low_less8(x0), e1 = high_less8(x0), e2 = low_less8(x1), e3 = high_less8(x1);
 #pragma unroll
                     for (int n = 0; n < NT; n++) {
-                        const uint32_t b0 = pack_bf16(s[2 * c2][2 * n] * s0, s[2 * c2][2 * n + 1] * s1);
-                        const uint32_t b1 = pack_bf16(s[2 * c2 + 1][2 * n] * s2, s[2 * c2 + 1][2 * n + 1] * s3);
+                        float p0, p1, p2, p3;
+                        mul2(F2(s[2 * c2][2 * n], s[2 * c2][2 * n + 1]), s0).get(p0, p1);
+                        mul2(F2(s[2 * c2 + 1][2 * n], s[2 * c2 + 1][2 * n + 1]), s1).get(p2, p3);
+                        const uint32_t b0 = pack_bf16(p0, p1), b1 = pack_bf16(p2, p3);
                         mma_bf16(o[n][2 * i], a0, a1, a2, a3, b0, b1);
                         mma_bf16(o[n][2 * i + 1], e0, e1, e2, e3, b0, b1);
                     }
