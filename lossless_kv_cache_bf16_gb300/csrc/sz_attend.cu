@@ -16,15 +16,13 @@
 // queries are scaled to 2^120 and weights by 2^92 beforehand (exactly), which
 // keeps products normal fp32 numbers.
 //
-//   S = Q K^T   A = query heads (rows g, g + 8), B = K codes (column = token).
-//               Each group of 32 channels sums into its own accumulator;
-//               -8 sum(q) takes the codes' offset of 8 away, and the group's
-//               scale multiplies the rest.
+//   S = K Q^T   A = K codes (row = token), B = queries (column = head).  Each
+//               group of 32 channels sums into its own accumulator; -8 sum(q)
+//               takes the codes' offset of 8 away, and the group's scale
+//               multiplies the rest.
 //   O = V^T P   A = V codes less 8 (one packed add, exact; row = channel),
 //               B = weight times the group's scale, rounded to bf16 once
-//               (column = head).
-// The S accumulator's layout is the B operand's layout, so the weights never
-// leave their thread.
+//               (column = head), turned from S's layout into B's by movmatrix.
 //
 // Work split.  The list of (sequence, kv head, unit of 32 tokens), with
 // kItemCost more entries per (sequence, kv head) for its fixed cost, is cut
@@ -51,11 +49,11 @@ constexpr uint32_t kMinShare = 4;  // list entries of a warp, at least
 
 template <int D, int NT>
 struct Shape {
-    static constexpr int kWarps = NT == 1 ? 16 : 8;
+    static constexpr int kWarps = NT == 1 ? 12 : 8;
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kHeads = 8 * NT;
     static constexpr uint32_t kUnitBytes = 2 * Cell<D>::kBytes;
-    static constexpr int kStages = (NT == 1 ? 2 : 4) * (D == 64 ? 2 : 1);
+    static constexpr int kStages = (NT == 1 ? 3 : 4) * (D == 64 ? 2 : 1);
     static constexpr int kRow = D + 4;  // floats of a head's row of a piece, padded against bank conflicts
     static constexpr uint32_t kPieceBytes = 4 * kHeads * kRow + 8 * kHeads;
     static constexpr uint32_t kRingBytes = kStages * kUnitBytes;  // of a warp
@@ -101,16 +99,16 @@ __device__ __forceinline__ F2 add2(F2 a, F2 b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(a.v) : "l"(a.v), "l"(b.v));
     return a;
 }
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(a.v) : "l"(a.v), "l"(b.v));
-    return a;
+// One of two packed bf16 as a float: sel is 0x1044 for the low one, 0x3244 for
+// the high one.
+__device__ __forceinline__ float scale_of(uint32_t w, uint32_t sel) { return __uint_as_float(prmt(w, 0u, sel)); }
+// Transposes an 8 x 8 matrix of 16-bit values, of which lane 4 r + c holds
+// columns 2 c and 2 c + 1 of row r.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
 }
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(a.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-    return a;
-}
-// Two packed bf16 as floats.
-__device__ __forceinline__ F2 unpack_bf16(uint32_t w) { return F2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)); }
 __device__ __forceinline__ float exp2_fast(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -252,48 +250,48 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attend_kernel(const
             }
         }
     };
-    // Tokens and page of this lane's cell (lanes 0 and 1) of unit nxt, fetched
-    // one unit ahead of its copies.
-    int32_t page = 0;
-    uint32_t tokens = 0;
+    // Units are looked up 16 at a time, within an item: lane j holds the
+    // address and the token count of cell j.
+    const uint8_t* src = nullptr;
+    uint32_t tokens = 0, batch_mask = 0, batch_units = 0, batch_at = 0;
     uint32_t in_flight = 0;  // stages issued and not yet waited for
     auto look_up = [&]() {
+        batch_at = batch_units = 0;
         settle();
+        if (!nxt_left) return;
+        batch_units = min(min(nxt_left, s_cost[nxt.b] - nxt.at), 16u);
+        const uint32_t first = (nxt.at - kItemCost) * kUnitTokens + lane * kCellTokens;
+        const uint32_t len = (uint32_t)p.lens[nxt.b];
         tokens = 0;
-        if (nxt_left && lane < 2) {
-            const uint32_t first = (nxt.at - kItemCost) * kUnitTokens + lane * kCellTokens;
-            const uint32_t len = (uint32_t)p.lens[nxt.b];
-            if (first < len) {
+        if (lane < 2 * batch_units && first < len) {
+            const int32_t page = p.table[(uint64_t)nxt.b * p.table_width + (first >> lg_page)];
+            if ((uint32_t)page < p.pool.pages) {
                 tokens = min(len - first, kCellTokens);
-                page = p.table[(uint64_t)nxt.b * p.table_width + (first >> lg_page)];
+                src = p.pool.base +
+                      cell_offset<D>(p.pool, (uint32_t)page, nxt.item / p.tiles, first & ((1u << lg_page) - 1u));
+            } else if (p.status) {
+                atomicMax(p.status, kStatusInvalid);
             }
         }
+        batch_mask = __ballot_sync(0xFFFFFFFFu, tokens != 0);
+        nxt.at += batch_units;
+        nxt_left -= batch_units;
     };
     auto issue = [&](uint32_t stage) {
-        if (nxt_left) {
-            if (tokens && (uint32_t)page >= p.pool.pages) {
-                if (p.status) atomicMax(p.status, kStatusInvalid);
-                tokens = 0;
-            }
-            const uint32_t cells = __popc(__ballot_sync(0xFFFFFFFFu, lane < 2 && tokens > 0));
-            if (lane == 0) mbar_arrive_expect_tx(&bars[stage], cells * C::kBytes);
-            if (lane < 2) counts[2 * stage + lane] = tokens;
-            __syncwarp();
-            if (lane < 2 && tokens) {
-                const uint32_t off = ((nxt.at - kItemCost) * kUnitTokens + lane * kCellTokens) & ((1u << lg_page) - 1u);
-                bulk_g2s(ring + stage * Sh::kUnitBytes + lane * C::kBytes,
-                         p.pool.base + cell_offset<D>(p.pool, (uint32_t)page, nxt.item / p.tiles, off), C::kBytes,
-                         &bars[stage]);
-            }
-            in_flight++;
-            nxt.at++;
-            nxt_left--;
-            look_up();
-        }
+        if (batch_at == batch_units) look_up();
+        if (batch_units == 0) return;
+        const bool mine = (lane >> 1) == batch_at;
+        if (lane == 0) mbar_arrive_expect_tx(&bars[stage], __popc(batch_mask >> (2 * batch_at) & 3u) * C::kBytes);
+        if (mine) counts[2 * stage + (lane & 1u)] = tokens;
+        __syncwarp();
+        if (mine && tokens)
+            bulk_g2s(ring + stage * Sh::kUnitBytes + (lane & 1u) * C::kBytes, src, C::kBytes, &bars[stage]);
+        in_flight++;
+        batch_at++;
     };
-    look_up();
 #pragma unroll 1
     for (int k = 0; k < Sh::kStages; k++) issue(k);
+    const uint32_t half_sel = g & 1u ? 0x3244u : 0x1044u;  // scales come in pairs of tokens
     uint32_t stage = 0, phase = 0;
     bool alive = true;  // false once a wait has given up: the rest is left out
 
@@ -311,8 +309,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attend_kernel(const
         const uint32_t heads = min((uint32_t)Sh::kHeads, p.group - tile * Sh::kHeads);
 
         // ---- query operands ----
-        uint32_t qa[kSteps][2 * NT];
-        float bias[kG][NT], mult[NT];
+        uint32_t qb[kSteps][NT][2];
+        float bias[kG][NT][2], mult[NT][2];  // of heads 2t and 2t + 1
 #pragma unroll
         for (int n = 0; n < NT; n++) {
             const uint32_t h = g + 8 * n;
@@ -345,7 +343,9 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attend_kernel(const
             const int up = (int)max(top >> 7, 1u) - 127;
             const float up1 = copysignf(__uint_as_float((uint32_t)(min(120 - up, 120) + 127) << 23), p.scale_log2);
             const float up2 = __uint_as_float((uint32_t)(max(-up, 0) + 127) << 23);
-            mult[n] = ldexpf(fabsf(p.scale_log2), 13 + up);
+            const float factor = ldexpf(fabsf(p.scale_log2), 13 + up);
+            mult[n][0] = __shfl_sync(0xFFFFFFFFu, factor, 8 * t);
+            mult[n][1] = __shfl_sync(0xFFFFFFFFu, factor, 8 * t + 4);
 #pragma unroll
             for (int i = 0; i < kG; i++) {
                 float v[8], sum = 0.f;
@@ -357,22 +357,24 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attend_kernel(const
                 }
                 sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
                 sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
-                bias[i][n] = sum * -__uint_as_float(1u << 19);  // 8 * 2^-133
-                // Operand pair e: channels (e, 4 + e) of this thread's 8; odd
-                // e meets codes times 16.
-                qa[2 * i][n] = pack_bf16(v[0], v[4]);
-                qa[2 * i][NT + n] = pack_bf16(v[1] * 0.0625f, v[5] * 0.0625f);
-                qa[2 * i + 1][n] = pack_bf16(v[2], v[6]);
-                qa[2 * i + 1][NT + n] = pack_bf16(v[3] * 0.0625f, v[7] * 0.0625f);
+                sum *= -__uint_as_float(1u << 19);  // 8 * 2^-133
+                bias[i][n][0] = __shfl_sync(0xFFFFFFFFu, sum, 8 * t);
+                bias[i][n][1] = __shfl_sync(0xFFFFFFFFu, sum, 8 * t + 4);
+                // Operand e: channels (e, 4 + e) of this thread's 8; odd e
+                // meets codes times 16.
+                qb[2 * i][n][0] = pack_bf16(v[0], v[4]);
+                qb[2 * i][n][1] = pack_bf16(v[1] * 0.0625f, v[5] * 0.0625f);
+                qb[2 * i + 1][n][0] = pack_bf16(v[2], v[6]);
+                qb[2 * i + 1][n][1] = pack_bf16(v[3] * 0.0625f, v[7] * 0.0625f);
             }
         }
 
         float o[NT][2 * kG][4];
-        float m[NT], l[NT];  // l: this thread's share of the sum of weights
+        float m[NT][2], l[NT][2];  // of heads 2t and 2t + 1; l: this thread's share of the sum of weights
 #pragma unroll
         for (int n = 0; n < NT; n++) {
-            m[n] = kNegInf;
-            l[n] = 0.f;
+            m[n][0] = m[n][1] = kNegInf;
+            l[n][0] = l[n][1] = 0.f;
 #pragma unroll
             for (int j = 0; j < 2 * kG; j++)
 #pragma unroll
@@ -395,127 +397,144 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attend_kernel(const
             }
             if (!alive) break;
             const uint8_t* u = ring + stage * Sh::kUnitBytes;
-            const uint32_t n0 = counts[2 * stage], n1 = counts[2 * stage + 1];
-            const bool whole = n0 == kCellTokens && n1 == kCellTokens;
-            // S of 32 tokens: 4 tiles of 8.
-            float s[4][2 * NT];
+            const uint2 held = *reinterpret_cast<const uint2*>(counts + 2 * stage);  // tokens of the two cells
+            const bool whole = held.x == kCellTokens && held.y == kCellTokens;
+            // S: s[n][c][2 r + k] is token 16 c + 8 r + g, head 8 n + 2 t + k.
+            float s[NT][2][4];
 #pragma unroll
-            for (int nb = 0; nb < 4; nb++) {
-                const uint8_t* cell = u + (nb >> 1) * C::kBytes;
-                uint32_t kw[kG], sw[kG];
-                lds_words<kG>(cell + ((nb & 1) * 8 + g) * (D / 2) + t * (4 * kG), kw);
-                lds_words<kG>(cell + 2 * C::kKScale + ((nb & 1) * 4 + t) * (4 * kG), sw);
-                F2 sum[2] = {F2(0.f, 0.f), F2(0.f, 0.f)};
+            for (int c = 0; c < 2; c++) {
+                const uint8_t* cell = u + c * C::kBytes;
+                uint32_t k0[kG], k1[kG], s0[kG], s1[kG];
+                lds_words<kG>(cell + (4 * g + t) * (4 * kG), k0);
+                lds_words<kG>(cell + (32 + 4 * g + t) * (4 * kG), k1);
+                lds_words<kG>(cell + 2 * C::kKScale + (g >> 1) * (4 * kG), s0);
+                lds_words<kG>(cell + 2 * C::kKScale + (4 + (g >> 1)) * (4 * kG), s1);
+#pragma unroll
+                for (int n = 0; n < NT; n++)
+#pragma unroll
+                    for (int k = 0; k < 4; k++) s[n][c][k] = 0.f;
 #pragma unroll
                 for (int i = 0; i < kG; i++) {
-                    float c[4];
-                    const uint32_t w = kw[i], w8 = kw[i] >> 8;
-                    mma_bf16_first(c, qa[2 * i][0], NT == 2 ? qa[2 * i][NT - 1] : 0u, qa[2 * i][NT],
-                                   NT == 2 ? qa[2 * i][2 * NT - 1] : 0u, w & 0x000F000Fu, w & 0x00F000F0u);
-                    mma_bf16(c, qa[2 * i + 1][0], NT == 2 ? qa[2 * i + 1][NT - 1] : 0u, qa[2 * i + 1][NT],
-                             NT == 2 ? qa[2 * i + 1][2 * NT - 1] : 0u, w8 & 0x000F000Fu, w8 & 0x00F000F0u);
-                    const F2 scale = unpack_bf16(sw[i]);
+                    const uint32_t x0 = k0[i] >> 8, x1 = k1[i] >> 8;
+                    const uint32_t a0 = k0[i] & 0x000F000Fu, a1 = k1[i] & 0x000F000Fu;
+                    const uint32_t a2 = k0[i] & 0x00F000F0u, a3 = k1[i] & 0x00F000F0u;
+                    const uint32_t e0 = x0 & 0x000F000Fu, e1 = x1 & 0x000F000Fu;
+                    const uint32_t e2 = x0 & 0x00F000F0u, e3 = x1 & 0x00F000F0u;
+                    const float f0 = scale_of(s0[i], half_sel), f1 = scale_of(s1[i], half_sel);
 #pragma unroll
-                    for (int n = 0; n < NT; n++)
-                        sum[n] = fma2(add2(F2(c[2 * n], c[2 * n + 1]), F2(bias[i][n], bias[i][n])), scale, sum[n]);
+                    for (int n = 0; n < NT; n++) {
+                        float d[4];
+                        mma_bf16_first(d, a0, a1, a2, a3, qb[2 * i][n][0], qb[2 * i][n][1]);
+                        mma_bf16(d, e0, e1, e2, e3, qb[2 * i + 1][n][0], qb[2 * i + 1][n][1]);
+                        const F2 off(bias[i][n][0], bias[i][n][1]);
+                        add2(F2(d[0], d[1]), off).get(d[0], d[1]);
+                        add2(F2(d[2], d[3]), off).get(d[2], d[3]);
+                        s[n][c][0] = fmaf(d[0], f0, s[n][c][0]);
+                        s[n][c][1] = fmaf(d[1], f0, s[n][c][1]);
+                        s[n][c][2] = fmaf(d[2], f1, s[n][c][2]);
+                        s[n][c][3] = fmaf(d[3], f1, s[n][c][3]);
+                    }
                 }
-#pragma unroll
-                for (int n = 0; n < NT; n++) sum[n].get(s[nb][2 * n], s[nb][2 * n + 1]);
             }
             if (!whole) {
 #pragma unroll
-                for (int nb = 0; nb < 4; nb++)
+                for (int n = 0; n < NT; n++)
 #pragma unroll
-                    for (int k = 0; k < 2 * NT; k++)
-                        if ((nb & 1) * 8 + 2 * t + (k & 1) >= (nb >> 1 ? n1 : n0)) s[nb][k] = kNegInf;
+                    for (int k = 0; k < 4; k++) {
+                        if (8 * (k >> 1) + g >= held.x) s[n][0][k] = kNegInf;
+                        if (8 * (k >> 1) + g >= held.y) s[n][1][k] = kNegInf;
+                    }
             }
             if (LOGITS) {
 #pragma unroll
-                for (int n = 0; n < NT; n++)
-                    if (g + 8 * n < heads) {
-                        const uint64_t tok = (uint64_t)unit * kUnitTokens;
-                        float* row = p.logits + ((uint64_t)seq * q_heads + head0 + g + 8 * n) * max_tokens + tok + 2 * t;
+                for (int n = 0; n < NT; n++) {
+                    const uint32_t h = 8 * n + 2 * t;
+                    float* row = p.logits + ((uint64_t)seq * q_heads + head0 + h) * max_tokens + (uint64_t)unit * kUnitTokens + g;
+                    const bool both = (uint64_t)unit * kUnitTokens + kCellTokens < max_tokens;
 #pragma unroll
-                        for (int nb = 0; nb < 4; nb++)
-                            if (nb < 2 || tok + kCellTokens < max_tokens)
-                                *reinterpret_cast<float2*>(row + 8 * nb) = make_float2(s[nb][2 * n] * mult[n], s[nb][2 * n + 1] * mult[n]);
+                    for (int k = 0; k < 4; k++) {
+                        if (h + (k & 1) >= heads) continue;
+                        float* dst = row + (k & 1) * max_tokens + 8 * (k >> 1);
+                        dst[0] = s[n][0][k] * mult[n][k & 1];
+                        if (both) dst[kCellTokens] = s[n][1][k] * mult[n][k & 1];
                     }
+                }
             }
-            // Running maximum, moved only when a row outgrows it by 2^8:
+            // Running maximum, moved only when a head outgrows it by 2^8:
             // weights stay at most 2^(92 + 8).
-            float top[NT];
+            float top[NT][2];
             bool grow = false;
 #pragma unroll
-            for (int n = 0; n < NT; n++) {
-                top[n] = fmaxf(s[0][2 * n], s[0][2 * n + 1]);
+            for (int n = 0; n < NT; n++)
 #pragma unroll
-                for (int nb = 1; nb < 4; nb++) top[n] = fmaxf(top[n], fmaxf(s[nb][2 * n], s[nb][2 * n + 1]));
-                top[n] = fmaxf(top[n], __shfl_xor_sync(0xFFFFFFFFu, top[n], 1));
-                top[n] = fmaxf(top[n], __shfl_xor_sync(0xFFFFFFFFu, top[n], 2));
-                top[n] = top[n] == kNegInf ? kNegInf : top[n] * mult[n];
-                grow |= top[n] > m[n] + 8.f;
-            }
+                for (int k = 0; k < 2; k++) {
+                    float x = fmaxf(fmaxf(s[n][0][k], s[n][0][k + 2]), fmaxf(s[n][1][k], s[n][1][k + 2]));
+                    x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 4));
+                    x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 8));
+                    x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));
+                    top[n][k] = x == kNegInf ? kNegInf : x * mult[n][k];
+                    grow |= top[n][k] > m[n][k] + 8.f;
+                }
             if (__any_sync(0xFFFFFFFFu, grow)) {
 #pragma unroll
                 for (int n = 0; n < NT; n++) {
-                    const float to = top[n] > m[n] + 8.f ? top[n] : m[n];
-                    const float f = exp2_fast(m[n] - or_zero(to));
-                    m[n] = to;
-                    l[n] *= f;
-                    // Heads 2t and 2t + 1 are this thread's columns of O.
-                    const float f0 = __shfl_sync(0xFFFFFFFFu, f, 8 * t), f1 = __shfl_sync(0xFFFFFFFFu, f, 8 * t + 4);
+                    float f[2];
+#pragma unroll
+                    for (int k = 0; k < 2; k++) {
+                        const float to = top[n][k] > m[n][k] + 8.f ? top[n][k] : m[n][k];
+                        f[k] = exp2_fast(m[n][k] - or_zero(to));
+                        m[n][k] = to;
+                        l[n][k] *= f[k];
+                    }
 #pragma unroll
                     for (int j = 0; j < 2 * kG; j++) {
-                        o[n][j][0] *= f0, o[n][j][1] *= f1;
-                        o[n][j][2] *= f0, o[n][j][3] *= f1;
+                        o[n][j][0] *= f[0], o[n][j][1] *= f[1];
+                        o[n][j][2] *= f[0], o[n][j][3] *= f[1];
                     }
                 }
             }
 #pragma unroll
-            for (int n = 0; n < NT; n++) {
-                const float ref = kWeightShift - or_zero(m[n]);
+            for (int n = 0; n < NT; n++)
 #pragma unroll
-                for (int nb = 0; nb < 4; nb++) {
-                    s[nb][2 * n] = exp2_fast(fmaf(s[nb][2 * n], mult[n], ref));
-                    s[nb][2 * n + 1] = exp2_fast(fmaf(s[nb][2 * n + 1], mult[n], ref));
-                    if (!whole) {  // minus infinity times a factor of 0 is no number
-                        const uint32_t held = nb >> 1 ? n1 : n0, at = (nb & 1) * 8 + 2 * t;
-                        if (at >= held) s[nb][2 * n] = 0.f;
-                        if (at + 1 >= held) s[nb][2 * n + 1] = 0.f;
-                    }
-                    l[n] += s[nb][2 * n] + s[nb][2 * n + 1];
+                for (int k = 0; k < 2; k++) {
+                    const float ref = kWeightShift - or_zero(m[n][k]);
+#pragma unroll
+                    for (int c = 0; c < 2; c++)
+#pragma unroll
+                        for (int r = 0; r < 2; r++) {
+                            float& x = s[n][c][2 * r + k];
+                            x = exp2_fast(fmaf(x, mult[n][k], ref));
+                            // Minus infinity times a factor of 0 is no number.
+                            if (!whole && 8 * r + g >= (c ? held.y : held.x)) x = 0.f;
+                            l[n][k] += x;
+                        }
                 }
-            }
             // O += V^T P, 16 tokens (one cell) at a time.
 #pragma unroll
-            for (int c2 = 0; c2 < 2; c2++) {
-                const uint8_t* cell = u + c2 * C::kBytes;
+            for (int c = 0; c < 2; c++) {
+                const uint8_t* cell = u + c * C::kBytes;
                 uint32_t w0[kG], w1[kG], v0[kG], v1[kG];
-                lds_words<kG>(cell + 2 * C::kVScale + t * (4 * kG), v0);
-                lds_words<kG>(cell + 2 * C::kVScale + (4 + t) * (4 * kG), v1);
+                lds_words<kG>(cell + 2 * C::kVScale + (g >> 1) * (4 * kG), v0);
+                lds_words<kG>(cell + 2 * C::kVScale + (4 + (g >> 1)) * (4 * kG), v1);
                 lds_words<kG>(cell + 2 * C::kV + (g * 4 + t) * (4 * kG), w0);
                 lds_words<kG>(cell + 2 * C::kV + (32 + g * 4 + t) * (4 * kG), w1);
                 if (!whole) {
                     // Scales of slots that hold nothing may be anything: zero
                     // times infinity must not reach the sums.
-                    const uint32_t n = c2 ? n1 : n0;
-                    const uint32_t k0 = (2 * t < n ? 0xFFFFu : 0u) | (2 * t + 1 < n ? 0xFFFF0000u : 0u);
-                    const uint32_t k1 = (8 + 2 * t < n ? 0xFFFFu : 0u) | (9 + 2 * t < n ? 0xFFFF0000u : 0u);
+                    const uint32_t n = c ? held.y : held.x;
 #pragma unroll
-                    for (int i = 0; i < kG; i++) v0[i] &= k0, v1[i] &= k1;
+                    for (int i = 0; i < kG; i++) v0[i] = g < n ? v0[i] : 0u, v1[i] = 8 + g < n ? v1[i] : 0u;
                 }
 #pragma unroll
                 for (int i = 0; i < kG; i++) {
                     const uint32_t x0 = w0[i] >> 8, x1 = w1[i] >> 8;
-                    const F2 s0 = unpack_bf16(v0[i]), s1 = unpack_bf16(v1[i]);
                     const uint32_t a0 = low_less8(w0[i]), a1 = high_less8(w0[i]), a2 = low_less8(w1[i]), a3 = high_less8(w1[i]);
                     const uint32_t e0 = low_less8(x0), e1 = high_less8(x0), e2 = low_less8(x1), e3 = high_less8(x1);
+                    const float f0 = scale_of(v0[i], half_sel), f1 = scale_of(v1[i], half_sel);
 #pragma unroll
                     for (int n = 0; n < NT; n++) {
-                        float p0, p1, p2, p3;
-                        mul2(F2(s[2 * c2][2 * n], s[2 * c2][2 * n + 1]), s0).get(p0, p1);
-                        mul2(F2(s[2 * c2 + 1][2 * n], s[2 * c2 + 1][2 * n + 1]), s1).get(p2, p3);
-                        const uint32_t b0 = pack_bf16(p0, p1), b1 = pack_bf16(p2, p3);
+                        const uint32_t b0 = transpose8x8(pack_bf16(s[n][c][0] * f0, s[n][c][1] * f0));
+                        const uint32_t b1 = transpose8x8(pack_bf16(s[n][c][2] * f1, s[n][c][3] * f1));
                         mma_bf16(o[n][2 * i], a0, a1, a2, a3, b0, b1);
                         mma_bf16(o[n][2 * i + 1], e0, e1, e2, e3, b0, b1);
                     }
@@ -535,18 +554,21 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attend_kernel(const
         if (!starts || !ends) __syncwarp();
 #pragma unroll
         for (int n = 0; n < NT; n++) {
-            l[n] += __shfl_xor_sync(0xFFFFFFFFu, l[n], 1);
-            l[n] += __shfl_xor_sync(0xFFFFFFFFu, l[n], 2);
-            l[n] *= 2.0194839173657902e-28f;
+#pragma unroll
+            for (int k = 0; k < 2; k++) {
+                l[n][k] += __shfl_xor_sync(0xFFFFFFFFu, l[n][k], 4);
+                l[n][k] += __shfl_xor_sync(0xFFFFFFFFu, l[n][k], 8);
+                l[n][k] += __shfl_xor_sync(0xFFFFFFFFu, l[n][k], 16);
+                l[n][k] *= 2.0194839173657902e-28f;
+            }
 #pragma unroll
             for (int j = 0; j < 2 * kG; j++) {
                 o[n][j][0] *= 2199023255552.f, o[n][j][1] *= 2199023255552.f;
                 o[n][j][2] *= 137438953472.f, o[n][j][3] *= 137438953472.f;
             }
-            const float l0 = __shfl_sync(0xFFFFFFFFu, l[n], 8 * t), l1 = __shfl_sync(0xFFFFFFFFu, l[n], 8 * t + 4);
             const uint32_t h = 8 * n + 2 * t;
             if (starts && ends) {
-                const float i0 = 1.f / l0, i1 = 1.f / l1;
+                const float i0 = 1.f / l[n][0], i1 = 1.f / l[n][1];
                 uint16_t* dst = p.out + (int64_t)seq * p.out_seq + (int64_t)(head0 + h) * p.out_head + 4 * g;
 #pragma unroll
                 for (int i = 0; i < kG; i++) {
@@ -566,16 +588,16 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attend_kernel(const
                         }
                     }
                 }
-                if (t == 0 && g + 8 * n < heads) {
-                    const uint64_t row = (uint64_t)seq * q_heads + head0 + g + 8 * n;
-                    const float lse2 = m[n] + log2f(l[n]);
+                if (g < 2 && h + g < heads) {
+                    const uint64_t row = (uint64_t)seq * q_heads + head0 + h + g;
+                    const float lse2 = g ? m[n][1] + log2f(l[n][1]) : m[n][0] + log2f(l[n][0]);
                     if (p.lse) p.lse[row] = lse2 * 0.6931471805599453f;
                     if (LOGITS) p.lse2[row] = lse2;
                 }
             } else {
-                if (t == 0) {
+                if (g < 2) {
                     float2* ml = reinterpret_cast<float2*>(piece + Sh::kHeads * Sh::kRow);
-                    ml[g + 8 * n] = make_float2(m[n], l[n]);
+                    ml[h + g] = g ? make_float2(m[n][1], l[n][1]) : make_float2(m[n][0], l[n][0]);
                 }
 #pragma unroll
                 for (int i = 0; i < kG; i++) {
