@@ -31,6 +31,8 @@
 // and writes the rows of an item that it holds whole.  Pieces of an item are
 // joined once per block in shared memory, pieces over several blocks by a
 // second kernel, both in list order: results do not depend on timing.
+#include <type_traits>
+
 #include "sz_cache.cuh"
 #include "sz_params.h"
 #include "sz_pipeline.cuh"
@@ -45,7 +47,7 @@ constexpr float kNegInf = -__builtin_huge_valf();
 // after the factor 2^-133 of the codes.
 constexpr float kWeightShift = 92.f;
 constexpr uint32_t kItemCost = 2;
-constexpr uint32_t kMinShare = 4;  // list entries of a warp, at least
+constexpr uint32_t kMinShare = 1;  // list entries of a warp, at least
 
 template <int D, int NT>
 struct Shape {
@@ -58,8 +60,8 @@ struct Shape {
     static constexpr uint32_t kPieceBytes = 4 * kHeads * kRow + 8 * kHeads;
     static constexpr uint32_t kRingBytes = kStages * kUnitBytes;  // of a warp
     static constexpr uint32_t kPiece = kWarps * kRingBytes;
-    static constexpr uint32_t kCost = kPiece + kWarps * kPieceBytes;
-    static constexpr uint32_t kBar = kCost + 4u * kMaxBatch;
+    static constexpr uint32_t kLen = kPiece + kWarps * kPieceBytes;
+    static constexpr uint32_t kBar = kLen + 4u * kMaxBatch;
     static constexpr uint32_t kCount = kBar + 8u * kWarps * kStages;
     static constexpr uint32_t kBytes = kCount + 8u * kWarps * kStages;
     static_assert(kBytes + 1024 <= 232448, "shared memory of a block");
@@ -137,18 +139,28 @@ __device__ __forceinline__ void lds_words(const uint8_t* p, uint32_t (&w)[N]) {
     }
 }
 
+// 64-bit division, in 32 bits where the numbers are that small.
+__device__ __forceinline__ uint64_t divide(uint64_t a, uint64_t b) {
+    return (a | b) >> 32 ? a / b : (uint32_t)a / (uint32_t)b;
+}
+
+// Entries of an item of a sequence of len tokens, 0 for an empty one.
+__device__ __forceinline__ uint32_t entries(uint32_t len) {
+    return len ? (len + kUnitTokens - 1) / kUnitTokens + kItemCost : 0u;
+}
+
 // A place in the list: sequence, item (kv head and tile of query heads) and
 // entry of the item, of which the first kItemCost stand for its fixed cost;
-// cost[b] is the number of entries of sequence b's items, 0 for an empty one.
+// len[b] is sequence b's length.
 struct Cursor {
     uint32_t b, item, at;
-    __device__ __forceinline__ void next_item(uint32_t items, const uint32_t* cost, uint32_t batch) {
+    __device__ __forceinline__ void next_item(uint32_t items, const uint32_t* len, uint32_t batch) {
         at = 0;
         if (++item == items) {
             item = 0;
             do {
                 b++;
-            } while (b < batch && cost[b] == 0);
+            } while (b < batch && len[b] == 0);
         }
     }
 };
@@ -159,7 +171,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attend_kernel(const
     using C = Cell<D>;
     constexpr int W = Sh::kWarps, kG = C::kGroups, kSteps = D / 16;
     extern __shared__ __align__(128) uint8_t smem[];
-    uint32_t* s_cost = reinterpret_cast<uint32_t*>(smem + Sh::kCost);
+    uint32_t* s_len = reinterpret_cast<uint32_t*>(smem + Sh::kLen);
     __shared__ uint32_t s_sum[W];
     __shared__ Left s_left[W];
     const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31u, g = lane >> 2, t = lane & 3u;
@@ -184,9 +196,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attend_kernel(const
         const int32_t len = p.lens[b];
         const bool ok = len >= 0 && (uint64_t)len <= max_tokens;
         if (!ok && p.status && blockIdx.x == 0) atomicMax(p.status, kStatusInvalid);
-        const uint32_t n = ok && len ? ((uint32_t)len + kUnitTokens - 1) / kUnitTokens + kItemCost : 0u;
-        s_cost[b] = n;
-        mine += n;
+        s_len[b] = ok ? (uint32_t)len : 0u;
+        mine += ok ? entries((uint32_t)len) : 0u;
     }
     mine = __reduce_add_sync(0xFFFFFFFFu, mine);
     if (lane == 0) s_sum[warp] = mine;
@@ -195,12 +206,12 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attend_kernel(const
     for (int w = 0; w < W; w++) total += s_sum[w];
     total *= items;
     const uint64_t workers = (uint64_t)gridDim.x * W;
-    const uint32_t share = (uint32_t)max((total + workers - 1) / workers, (uint64_t)kMinShare);
+    const uint32_t share = (uint32_t)max(divide(total + workers - 1, workers), (uint64_t)kMinShare);
     const uint64_t u0 = min(((uint64_t)blockIdx.x * W + warp) * share, total);
     const uint32_t n_run = (uint32_t)(min(u0 + share, total) - u0);
     // Rows of empty sequences are zero, with a log-sum of -infinity.
     for (uint32_t b = blockIdx.x; b < p.batch; b += gridDim.x) {
-        if (s_cost[b]) continue;
+        if (s_len[b]) continue;
         for (uint32_t x = tid; x < q_heads * D; x += Sh::kThreads)
             p.out[(int64_t)b * p.out_seq + (int64_t)(x / D) * p.out_head + x % D] = 0;
         for (uint32_t h = tid; h < q_heads; h += Sh::kThreads)
@@ -213,7 +224,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attend_kernel(const
     if (n_run) {
         uint64_t before = 0;
         for (uint32_t b0 = 0; b0 < p.batch; b0 += 32) {
-            const uint32_t n = b0 + lane < p.batch ? s_cost[b0 + lane] : 0u;
+            const uint32_t n = b0 + lane < p.batch ? entries(s_len[b0 + lane]) : 0u;
             uint32_t upto = n;
 #pragma unroll
             for (int d = 1; d < 32; d *= 2) {
@@ -226,7 +237,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attend_kernel(const
                 const int who = __ffs(past) - 1;
                 const uint32_t nb = __shfl_sync(0xFFFFFFFFu, n, who);
                 const uint64_t at = u0 - (__shfl_sync(0xFFFFFFFFu, end, who) - (uint64_t)nb * items);
-                cur = Cursor{b0 + (uint32_t)who, (uint32_t)(at / nb), (uint32_t)(at % nb)};
+                const uint32_t item = (uint32_t)divide(at, nb);
+                cur = Cursor{b0 + (uint32_t)who, item, (uint32_t)(at - (uint64_t)item * nb)};
                 break;
             }
             before = __shfl_sync(0xFFFFFFFFu, end, 31);
@@ -243,8 +255,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attend_kernel(const
                 const uint32_t skip = min(kItemCost - nxt.at, nxt_left);
                 nxt.at += skip;
                 nxt_left -= skip;
-            } else if (nxt.at >= s_cost[nxt.b]) {
-                nxt.next_item(items, s_cost, p.batch);
+            } else if (nxt.at >= entries(s_len[nxt.b])) {
+                nxt.next_item(items, s_len, p.batch);
             } else {
                 break;
             }
@@ -259,9 +271,9 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attend_kernel(const
         batch_at = batch_units = 0;
         settle();
         if (!nxt_left) return;
-        batch_units = min(min(nxt_left, s_cost[nxt.b] - nxt.at), 16u);
+        batch_units = min(min(nxt_left, entries(s_len[nxt.b]) - nxt.at), 16u);
         const uint32_t first = (nxt.at - kItemCost) * kUnitTokens + lane * kCellTokens;
-        const uint32_t len = (uint32_t)p.lens[nxt.b];
+        const uint32_t len = s_len[nxt.b];
         tokens = 0;
         if (lane < 2 * batch_units && first < len) {
             const int32_t page = p.table[(uint64_t)nxt.b * p.table_width + (first >> lg_page)];
@@ -296,12 +308,12 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attend_kernel(const
     bool alive = true;  // false once a wait has given up: the rest is left out
 
     for (uint32_t left = n_run; left;) {
-        const uint32_t cost = s_cost[cur.b], take = min(left, cost - cur.at);
+        const uint32_t cost = entries(s_len[cur.b]), take = min(left, cost - cur.at);
         const uint32_t r0 = max(cur.at, kItemCost) - kItemCost, r1 = max(cur.at + take, kItemCost) - kItemCost;
         const uint32_t seq = cur.b, item = cur.item;
         left -= take;
         cur.at += take;
-        if (cur.at == cost) cur.next_item(items, s_cost, p.batch);
+        if (cur.at == cost) cur.next_item(items, s_len, p.batch);
         if (r0 == r1) continue;
         const bool starts = r0 == 0, ends = r1 == cost - kItemCost;
         const uint32_t kv_head = item / p.tiles, tile = item % p.tiles;
@@ -398,148 +410,155 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attend_kernel(const
             if (!alive) break;
             const uint8_t* u = ring + stage * Sh::kUnitBytes;
             const uint2 held = *reinterpret_cast<const uint2*>(counts + 2 * stage);  // tokens of the two cells
-            const bool whole = held.x == kCellTokens && held.y == kCellTokens;
-            // S: s[n][c][2 r + k] is token 16 c + 8 r + g, head 8 n + 2 t + k.
-            float s[NT][2][4];
+            auto take_unit = [&](auto partial) {
+                constexpr bool PARTIAL = decltype(partial)::value;
+                // S: s[n][c][2 r + k] is token 16 c + 8 r + g, head 8 n + 2 t + k.
+                float s[NT][2][4];
 #pragma unroll
-            for (int c = 0; c < 2; c++) {
-                const uint8_t* cell = u + c * C::kBytes;
-                uint32_t k0[kG], k1[kG], s0[kG], s1[kG];
-                lds_words<kG>(cell + (4 * g + t) * (4 * kG), k0);
-                lds_words<kG>(cell + (32 + 4 * g + t) * (4 * kG), k1);
-                lds_words<kG>(cell + 2 * C::kKScale + (g >> 1) * (4 * kG), s0);
-                lds_words<kG>(cell + 2 * C::kKScale + (4 + (g >> 1)) * (4 * kG), s1);
+                for (int c = 0; c < 2; c++) {
+                    const uint8_t* cell = u + c * C::kBytes;
+                    uint32_t k0[kG], k1[kG], s0[kG], s1[kG];
+                    lds_words<kG>(cell + (4 * g + t) * (4 * kG), k0);
+                    lds_words<kG>(cell + (32 + 4 * g + t) * (4 * kG), k1);
+                    lds_words<kG>(cell + 2 * C::kKScale + (g >> 1) * (4 * kG), s0);
+                    lds_words<kG>(cell + 2 * C::kKScale + (4 + (g >> 1)) * (4 * kG), s1);
 #pragma unroll
-                for (int n = 0; n < NT; n++)
+                    for (int n = 0; n < NT; n++)
 #pragma unroll
-                    for (int k = 0; k < 4; k++) s[n][c][k] = 0.f;
+                        for (int k = 0; k < 4; k++) s[n][c][k] = 0.f;
 #pragma unroll
-                for (int i = 0; i < kG; i++) {
-                    const uint32_t x0 = k0[i] >> 8, x1 = k1[i] >> 8;
-                    const uint32_t a0 = k0[i] & 0x000F000Fu, a1 = k1[i] & 0x000F000Fu;
-                    const uint32_t a2 = k0[i] & 0x00F000F0u, a3 = k1[i] & 0x00F000F0u;
-                    const uint32_t e0 = x0 & 0x000F000Fu, e1 = x1 & 0x000F000Fu;
-                    const uint32_t e2 = x0 & 0x00F000F0u, e3 = x1 & 0x00F000F0u;
-                    const float f0 = scale_of(s0[i], half_sel), f1 = scale_of(s1[i], half_sel);
+                    for (int i = 0; i < kG; i++) {
+                        const uint32_t x0 = k0[i] >> 8, x1 = k1[i] >> 8;
+                        const uint32_t a0 = k0[i] & 0x000F000Fu, a1 = k1[i] & 0x000F000Fu;
+                        const uint32_t a2 = k0[i] & 0x00F000F0u, a3 = k1[i] & 0x00F000F0u;
+                        const uint32_t e0 = x0 & 0x000F000Fu, e1 = x1 & 0x000F000Fu;
+                        const uint32_t e2 = x0 & 0x00F000F0u, e3 = x1 & 0x00F000F0u;
+                        const float f0 = scale_of(s0[i], half_sel), f1 = scale_of(s1[i], half_sel);
 #pragma unroll
-                    for (int n = 0; n < NT; n++) {
-                        float d[4];
-                        mma_bf16_first(d, a0, a1, a2, a3, qb[2 * i][n][0], qb[2 * i][n][1]);
-                        mma_bf16(d, e0, e1, e2, e3, qb[2 * i + 1][n][0], qb[2 * i + 1][n][1]);
-                        const F2 off(bias[i][n][0], bias[i][n][1]);
-                        add2(F2(d[0], d[1]), off).get(d[0], d[1]);
-                        add2(F2(d[2], d[3]), off).get(d[2], d[3]);
-                        s[n][c][0] = fmaf(d[0], f0, s[n][c][0]);
-                        s[n][c][1] = fmaf(d[1], f0, s[n][c][1]);
-                        s[n][c][2] = fmaf(d[2], f1, s[n][c][2]);
-                        s[n][c][3] = fmaf(d[3], f1, s[n][c][3]);
+                        for (int n = 0; n < NT; n++) {
+                            float d[4];
+                            mma_bf16_first(d, a0, a1, a2, a3, qb[2 * i][n][0], qb[2 * i][n][1]);
+                            mma_bf16(d, e0, e1, e2, e3, qb[2 * i + 1][n][0], qb[2 * i + 1][n][1]);
+                            const F2 off(bias[i][n][0], bias[i][n][1]);
+                            add2(F2(d[0], d[1]), off).get(d[0], d[1]);
+                            add2(F2(d[2], d[3]), off).get(d[2], d[3]);
+                            s[n][c][0] = fmaf(d[0], f0, s[n][c][0]);
+                            s[n][c][1] = fmaf(d[1], f0, s[n][c][1]);
+                            s[n][c][2] = fmaf(d[2], f1, s[n][c][2]);
+                            s[n][c][3] = fmaf(d[3], f1, s[n][c][3]);
+                        }
                     }
                 }
-            }
-            if (!whole) {
+                if constexpr (PARTIAL) {
 #pragma unroll
-                for (int n = 0; n < NT; n++)
+                    for (int n = 0; n < NT; n++)
 #pragma unroll
-                    for (int k = 0; k < 4; k++) {
-                        if (8 * (k >> 1) + g >= held.x) s[n][0][k] = kNegInf;
-                        if (8 * (k >> 1) + g >= held.y) s[n][1][k] = kNegInf;
-                    }
-            }
-            if (LOGITS) {
-#pragma unroll
-                for (int n = 0; n < NT; n++) {
-                    const uint32_t h = 8 * n + 2 * t;
-                    float* row = p.logits + ((uint64_t)seq * q_heads + head0 + h) * max_tokens + (uint64_t)unit * kUnitTokens + g;
-                    const bool both = (uint64_t)unit * kUnitTokens + kCellTokens < max_tokens;
-#pragma unroll
-                    for (int k = 0; k < 4; k++) {
-                        if (h + (k & 1) >= heads) continue;
-                        float* dst = row + (k & 1) * max_tokens + 8 * (k >> 1);
-                        dst[0] = s[n][0][k] * mult[n][k & 1];
-                        if (both) dst[kCellTokens] = s[n][1][k] * mult[n][k & 1];
-                    }
-                }
-            }
-            // Running maximum, moved only when a head outgrows it by 2^8:
-            // weights stay at most 2^(92 + 8).
-            float top[NT][2];
-            bool grow = false;
-#pragma unroll
-            for (int n = 0; n < NT; n++)
-#pragma unroll
-                for (int k = 0; k < 2; k++) {
-                    float x = fmaxf(fmaxf(s[n][0][k], s[n][0][k + 2]), fmaxf(s[n][1][k], s[n][1][k + 2]));
-                    x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 4));
-                    x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 8));
-                    x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));
-                    top[n][k] = x == kNegInf ? kNegInf : x * mult[n][k];
-                    grow |= top[n][k] > m[n][k] + 8.f;
-                }
-            if (__any_sync(0xFFFFFFFFu, grow)) {
-#pragma unroll
-                for (int n = 0; n < NT; n++) {
-                    float f[2];
-#pragma unroll
-                    for (int k = 0; k < 2; k++) {
-                        const float to = top[n][k] > m[n][k] + 8.f ? top[n][k] : m[n][k];
-                        f[k] = exp2_fast(m[n][k] - or_zero(to));
-                        m[n][k] = to;
-                        l[n][k] *= f[k];
-                    }
-#pragma unroll
-                    for (int j = 0; j < 2 * kG; j++) {
-                        o[n][j][0] *= f[0], o[n][j][1] *= f[1];
-                        o[n][j][2] *= f[0], o[n][j][3] *= f[1];
-                    }
-                }
-            }
-#pragma unroll
-            for (int n = 0; n < NT; n++)
-#pragma unroll
-                for (int k = 0; k < 2; k++) {
-                    const float ref = kWeightShift - or_zero(m[n][k]);
-#pragma unroll
-                    for (int c = 0; c < 2; c++)
-#pragma unroll
-                        for (int r = 0; r < 2; r++) {
-                            float& x = s[n][c][2 * r + k];
-                            x = exp2_fast(fmaf(x, mult[n][k], ref));
-                            // Minus infinity times a factor of 0 is no number.
-                            if (!whole && 8 * r + g >= (c ? held.y : held.x)) x = 0.f;
-                            l[n][k] += x;
+                        for (int k = 0; k < 4; k++) {
+                            if (8 * (k >> 1) + g >= held.x) s[n][0][k] = kNegInf;
+                            if (8 * (k >> 1) + g >= held.y) s[n][1][k] = kNegInf;
                         }
                 }
-            // O += V^T P, 16 tokens (one cell) at a time.
-#pragma unroll
-            for (int c = 0; c < 2; c++) {
-                const uint8_t* cell = u + c * C::kBytes;
-                uint32_t w0[kG], w1[kG], v0[kG], v1[kG];
-                lds_words<kG>(cell + 2 * C::kVScale + (g >> 1) * (4 * kG), v0);
-                lds_words<kG>(cell + 2 * C::kVScale + (4 + (g >> 1)) * (4 * kG), v1);
-                lds_words<kG>(cell + 2 * C::kV + (g * 4 + t) * (4 * kG), w0);
-                lds_words<kG>(cell + 2 * C::kV + (32 + g * 4 + t) * (4 * kG), w1);
-                if (!whole) {
-                    // Scales of slots that hold nothing may be anything: zero
-                    // times infinity must not reach the sums.
-                    const uint32_t n = c ? held.y : held.x;
-#pragma unroll
-                    for (int i = 0; i < kG; i++) v0[i] = g < n ? v0[i] : 0u, v1[i] = 8 + g < n ? v1[i] : 0u;
-                }
-#pragma unroll
-                for (int i = 0; i < kG; i++) {
-                    const uint32_t x0 = w0[i] >> 8, x1 = w1[i] >> 8;
-                    const uint32_t a0 = low_less8(w0[i]), a1 = high_less8(w0[i]), a2 = low_less8(w1[i]), a3 = high_less8(w1[i]);
-                    const uint32_t e0 = low_less8(x0), e1 = high_less8(x0), e2 = low_less8(x1), e3 = high_less8(x1);
-                    const float f0 = scale_of(v0[i], half_sel), f1 = scale_of(v1[i], half_sel);
+                if (LOGITS) {
 #pragma unroll
                     for (int n = 0; n < NT; n++) {
-                        const uint32_t b0 = transpose8x8(pack_bf16(s[n][c][0] * f0, s[n][c][1] * f0));
-                        const uint32_t b1 = transpose8x8(pack_bf16(s[n][c][2] * f1, s[n][c][3] * f1));
-                        mma_bf16(o[n][2 * i], a0, a1, a2, a3, b0, b1);
-                        mma_bf16(o[n][2 * i + 1], e0, e1, e2, e3, b0, b1);
+                        const uint32_t h = 8 * n + 2 * t;
+                        float* row = p.logits + ((uint64_t)seq * q_heads + head0 + h) * max_tokens + (uint64_t)unit * kUnitTokens + g;
+                        const bool both = (uint64_t)unit * kUnitTokens + kCellTokens < max_tokens;
+#pragma unroll
+                        for (int k = 0; k < 4; k++) {
+                            if (h + (k & 1) >= heads) continue;
+                            float* dst = row + (k & 1) * max_tokens + 8 * (k >> 1);
+                            dst[0] = s[n][0][k] * mult[n][k & 1];
+                            if (both) dst[kCellTokens] = s[n][1][k] * mult[n][k & 1];
+                        }
                     }
                 }
-            }
+                // Running maximum, moved only when a head outgrows it by 2^8:
+                // weights stay at most 2^(92 + 8).
+                float top[NT][2];
+                bool grow = false;
+#pragma unroll
+                for (int n = 0; n < NT; n++)
+#pragma unroll
+                    for (int k = 0; k < 2; k++) {
+                        top[n][k] = fmaxf(fmaxf(s[n][0][k], s[n][0][k + 2]), fmaxf(s[n][1][k], s[n][1][k + 2]));
+                        grow |= top[n][k] * mult[n][k] > m[n][k] + 8.f;
+                    }
+                if (__any_sync(0xFFFFFFFFu, grow)) {
+#pragma unroll
+                    for (int n = 0; n < NT; n++) {
+                        float f[2];
+#pragma unroll
+                        for (int k = 0; k < 2; k++) {
+                            float x = top[n][k];
+                            x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 4));
+                            x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 8));
+                            x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));
+                            x *= mult[n][k];
+                            const float to = x > m[n][k] + 8.f ? x : m[n][k];
+                            f[k] = exp2_fast(m[n][k] - or_zero(to));
+                            m[n][k] = to;
+                            l[n][k] *= f[k];
+                        }
+#pragma unroll
+                        for (int j = 0; j < 2 * kG; j++) {
+                            o[n][j][0] *= f[0], o[n][j][1] *= f[1];
+                            o[n][j][2] *= f[0], o[n][j][3] *= f[1];
+                        }
+                    }
+                }
+#pragma unroll
+                for (int n = 0; n < NT; n++)
+#pragma unroll
+                    for (int k = 0; k < 2; k++) {
+                        const float ref = kWeightShift - or_zero(m[n][k]);
+#pragma unroll
+                        for (int c = 0; c < 2; c++)
+#pragma unroll
+                            for (int r = 0; r < 2; r++) {
+                                float& x = s[n][c][2 * r + k];
+                                x = exp2_fast(fmaf(x, mult[n][k], ref));
+                                // Minus infinity times a factor of 0 is no number.
+                                if (PARTIAL && 8 * r + g >= (c ? held.y : held.x)) x = 0.f;
+                                l[n][k] += x;
+                            }
+                    }
+                // O += V^T P, 16 tokens (one cell) at a time.
+#pragma unroll
+                for (int c = 0; c < 2; c++) {
+                    const uint8_t* cell = u + c * C::kBytes;
+                    uint32_t w0[kG], w1[kG], v0[kG], v1[kG];
+                    lds_words<kG>(cell + 2 * C::kVScale + (g >> 1) * (4 * kG), v0);
+                    lds_words<kG>(cell + 2 * C::kVScale + (4 + (g >> 1)) * (4 * kG), v1);
+                    lds_words<kG>(cell + 2 * C::kV + (g * 4 + t) * (4 * kG), w0);
+                    lds_words<kG>(cell + 2 * C::kV + (32 + g * 4 + t) * (4 * kG), w1);
+                    if constexpr (PARTIAL) {
+                        // Scales of slots that hold nothing may be anything: zero
+                        // times infinity must not reach the sums.
+                        const uint32_t n = c ? held.y : held.x;
+#pragma unroll
+                        for (int i = 0; i < kG; i++) v0[i] = g < n ? v0[i] : 0u, v1[i] = 8 + g < n ? v1[i] : 0u;
+                    }
+#pragma unroll
+                    for (int i = 0; i < kG; i++) {
+                        const uint32_t x0 = w0[i] >> 8, x1 = w1[i] >> 8;
+                        const uint32_t a0 = low_less8(w0[i]), a1 = high_less8(w0[i]), a2 = low_less8(w1[i]), a3 = high_less8(w1[i]);
+                        const uint32_t e0 = low_less8(x0), e1 = high_less8(x0), e2 = low_less8(x1), e3 = high_less8(x1);
+                        const float f0 = scale_of(v0[i], half_sel), f1 = scale_of(v1[i], half_sel);
+#pragma unroll
+                        for (int n = 0; n < NT; n++) {
+                            const uint32_t b0 = transpose8x8(pack_bf16(s[n][c][0] * f0, s[n][c][1] * f0));
+                            const uint32_t b1 = transpose8x8(pack_bf16(s[n][c][2] * f1, s[n][c][3] * f1));
+                            mma_bf16(o[n][2 * i], a0, a1, a2, a3, b0, b1);
+                            mma_bf16(o[n][2 * i + 1], e0, e1, e2, e3, b0, b1);
+                        }
+                    }
+                }
+            };
+            if (held.x == kCellTokens && held.y == kCellTokens)
+                take_unit(std::false_type{});
+            else
+                take_unit(std::true_type{});
             in_flight--;
             __syncwarp();
             issue(stage);
