@@ -370,7 +370,7 @@ sz_status sz_debug_encode_stalled(sz_dtype dt, const sz_codebook* h_cb, const vo
  * softmax statistics and norms are held in fp32.
  *
  * Strides are in elements; the head_dim channels of a row are contiguous.
- * 16-byte aligned rows (8-byte for append and read) take the vectorised path.
+ * 16-byte aligned rows take the vectorised path.
  *
  * The cache is a pool of pool_pages pages (16-byte aligned, page q at d_pool
  * + q * sz_cache_page_bytes).  page_tokens is a power of two in [16, 4096],

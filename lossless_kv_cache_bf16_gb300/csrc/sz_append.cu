@@ -1,14 +1,22 @@
 // sz_append.cu -- K and V rows into the 4-bit cache, and back.
 //
 // A group of 32 channels shares s = bf16(max|x| / 7); a channel's code is
-// 8 + round(x / s).  The quotient is correctly rounded (the product with the
-// reciprocal, corrected by its remainder, which fma gives exactly), so that
+// 8 + round(x / s).  The quotient is the product with the reciprocal,
+// corrected by its remainder, which fma gives exactly, so that
 // the codes are those of the definition: two bf16 significands have a
 // quotient that is k + 1/2 or at least 2^-17 away from it, which fp32 tells
-// apart.
+// apart.  |x / s| stays below 7.03, so that no code needs clamping, and the
+// sum of x / s and 1.5 * 2^23 + 8 holds the code in its low bits.
 //
-// A lane takes 4 channels of a row, 8 lanes a group; each lane's 4 codes are
-// one 16-bit word of the cell.
+// Bound by memory: 4 D bytes of rows and 9 D / 8 of cache per token and head.
+// A warp takes 8 tokens of one head, and its lanes are laid out as the cell
+// is, so that each moves whole 16-byte pieces of it (D = 128):
+//   K  lane 4 g + q: token g, channels 32 i + 8 q .. + 7 of every group i;
+//   V  lane 4 g + q: tokens 2 q and 2 q + 1, channels 32 i + 4 g .. + 3.
+// Two neighbouring tokens share the words of V's codes and of all scales.
+// Where their slots are not an even one and the next (scattered tokens, or a
+// run that starts at an odd slot after the first), their 16-bit words are
+// moved one by one.
 #include "sz_cache.cuh"
 #include "sz_params.h"
 
@@ -16,131 +24,307 @@ namespace sz {
 namespace {
 
 constexpr uint32_t kThreads = 256;
+constexpr uint32_t kTaskTokens = 8;
 
-__device__ __forceinline__ void load4(const uint16_t* p, bool vec, uint32_t (&x)[4]) {
+// N (4 or 8) bf16 bit patterns.
+template <int N>
+__device__ __forceinline__ void load_row(const uint16_t* p, bool vec, uint32_t (&x)[N]) {
     if (vec) {
-        const uint2 v = *reinterpret_cast<const uint2*>(p);
-        x[0] = v.x & 0xFFFFu, x[1] = v.x >> 16, x[2] = v.y & 0xFFFFu, x[3] = v.y >> 16;
+        uint32_t w[N / 2];
+        if constexpr (N == 8) {
+            const uint4 v = *reinterpret_cast<const uint4*>(p);
+            w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+        } else {
+            const uint2 v = *reinterpret_cast<const uint2*>(p);
+            w[0] = v.x, w[1] = v.y;
+        }
+#pragma unroll
+        for (int j = 0; j < N / 2; j++) x[2 * j] = w[j] & 0xFFFFu, x[2 * j + 1] = w[j] >> 16;
     } else {
 #pragma unroll
-        for (int j = 0; j < 4; j++) x[j] = p[j];
+        for (int j = 0; j < N; j++) x[j] = p[j];
     }
 }
 
-// The 4 codes of this lane's channels and, in every lane of the group, the
-// scale's bf16 bits.  All 32 lanes take part.
-__device__ __forceinline__ uint32_t quantise4(const uint32_t (&x)[4], uint32_t& scale) {
-    uint32_t top = 0;  // |x| as bf16 bits compares like the value; above 0x7F7F: infinity or NaN
+template <int N>
+__device__ __forceinline__ void store_row(uint16_t* p, bool vec, const float (&v)[N]) {
+    if (vec) {
+        if constexpr (N == 8)
+            *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
+                                                      pack_bf16(v[6], v[7]));
+        else
+            *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+    } else {
 #pragma unroll
-    for (int j = 0; j < 4; j++) top = max(top, x[j] & 0x7FFFu);
-#pragma unroll
-    for (uint32_t m = 1; m < 8; m *= 2) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, m));
-    scale = bf16_bits(__fdiv_rn(bf16_float(top), 7.f));
-    if (scale < 0x0080u) scale = 0;      // below 2^-126
-    if (top > 0x7F7Fu) scale = 0x7FC0u;  // NaN: the group reads as NaN
-    if (scale == 0 || top > 0x7F7Fu) return 0x8888u;
-    const float s = bf16_float(scale), inv = __frcp_rn(s);
+        for (int j = 0; j < N; j++) p[j] = (uint16_t)bf16_bits(v[j]);
+    }
+}
+
+__device__ __forceinline__ float reciprocal(float s) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+    return r;
+}
+// a / b for inv = 1 / b within 2^-22: the product's remainder is exact, so
+// that the sum has an error far below half a last place, and a quotient that
+// fp32 holds comes out exactly.
+__device__ __forceinline__ float quotient(float a, float b, float inv) {
+    const float q = __fmul_rn(a, inv);
+    return __fmaf_rn(__fmaf_rn(-q, b, a), inv, q);
+}
+
+// The scale's bf16 bits of a group whose largest |x| has the bits `top`:
+// 0 below 2^-126, a NaN for a group that holds an infinity or a NaN.
+__device__ __forceinline__ uint32_t scale_bits(uint32_t top) {
+    const uint32_t s = bf16_bits(quotient(bf16_float(top), 7.f, 1.f / 7.f));
+    return top > 0x7F7Fu ? 0x7FC0u : s < 0x0080u ? 0u : s;
+}
+
+// Codes of N values, 4 bits each, x[0] lowest.
+template <int N>
+__device__ __forceinline__ uint32_t codes_of(const uint32_t (&x)[N], uint32_t scale) {
+    const bool usable = scale - 1u < 0x7F7Fu;  // neither 0 nor a NaN
+    const float s = usable ? bf16_float(scale) : 1.f, inv = reciprocal(s);
     uint32_t w = 0;
 #pragma unroll
-    for (int j = 0; j < 4; j++) {
-        const float v = bf16_float(x[j]);
-        const float q0 = __fmul_rn(v, inv);
-        const float q = __fmaf_rn(__fmaf_rn(-q0, s, v), inv, q0);
-        const int c = max(-7, min(7, __float2int_rn(q)));
-        w |= (uint32_t)(c + 8) << (4 * j);
+    for (int j = N - 1; j >= 0; j--) {
+        const float q = quotient(bf16_float(x[j]), s, inv);
+        w = (w << 4) | (__float_as_uint(q + 12582920.f) & 15u);
     }
-    return w;
+    return usable ? w : 0x88888888u >> (32 - 4 * N);
 }
 
-// Where a slot lies, or false for one to leave out (-1, or outside the pool,
-// which is reported).
-__device__ __forceinline__ bool locate(const CachePool& c, int64_t slot, int* status, uint32_t& page, uint32_t& off) {
-    const int64_t limit = (int64_t)c.pages << c.lg_page;
-    if (slot < 0 || slot >= limit) {
-        if (slot != -1 && status) atomicMax(status, kStatusInvalid);
-        return false;
+template <int N>
+__device__ __forceinline__ uint32_t largest(const uint32_t (&x)[N]) {
+    uint32_t top = 0;  // |x| as bf16 bits compares like the value
+#pragma unroll
+    for (int j = 0; j < N; j++) top = max(top, x[j] & 0x7FFFu);
+    return top;
+}
+
+// A token's place: its cell (null where the token is left out: slot -1, or one
+// outside the pool, which is reported) and its number in the cell.
+struct Place {
+    uint16_t* cell;
+    uint32_t t;
+    uint64_t entry;  // of the tables beside the pool
+};
+
+template <int D>
+__device__ __forceinline__ Place locate(const AppendParams& p, int64_t token, uint32_t h) {
+    Place at{nullptr, 0, 0};
+    if (token < 0 || token >= (int64_t)p.tokens) return at;
+    const int64_t slot = p.slots[token];
+    if (slot < 0 || slot >= (int64_t)p.pool.pages << p.pool.lg_page) {
+        if (slot != -1 && p.status) atomicMax(p.status, kStatusInvalid);
+        return at;
     }
-    page = (uint32_t)(slot >> c.lg_page);
-    off = (uint32_t)slot & ((1u << c.lg_page) - 1u);
-    return true;
+    const uint32_t page = (uint32_t)(slot >> p.pool.lg_page), off = (uint32_t)slot & ((1u << p.pool.lg_page) - 1u);
+    at.cell = reinterpret_cast<uint16_t*>(p.pool.base + cell_offset<D>(p.pool, page, h, off));
+    at.t = off & 15u;
+    at.entry = (((uint64_t)page * p.pool.heads + h) << p.pool.lg_page) + off;
+    return at;
+}
+
+// Whether two tokens' words lie side by side.
+__device__ __forceinline__ bool side_by_side(const Place& a, const Place& b) {
+    return a.cell && a.cell == b.cell && !(a.t & 1u) && b.t == a.t + 1;
+}
+
+// N (2 or 4) words to or from an 8 N / 2 byte aligned place.
+template <int N>
+__device__ __forceinline__ void put_words(uint16_t* p, const uint32_t (&w)[N]) {
+    if constexpr (N == 4)
+        *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    else
+        *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+}
+template <int N>
+__device__ __forceinline__ void get_words(const uint16_t* p, uint32_t (&w)[N]) {
+    if constexpr (N == 4) {
+        const uint4 v = *reinterpret_cast<const uint4*>(p);
+        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    } else {
+        const uint2 v = *reinterpret_cast<const uint2*>(p);
+        w[0] = v.x, w[1] = v.y;
+    }
+}
+
+// Tasks of the call: 8 tokens of a head each.  The first task starts one
+// token early where the first slot is odd, so that pairs of a run are pairs
+// of slots.
+struct Task {
+    int64_t token;
+    uint32_t h;
+    __device__ __forceinline__ Task(const AppendParams& p, uint64_t n) {
+        h = (uint32_t)(n % p.pool.heads);
+        token = (int64_t)(n / p.pool.heads) * kTaskTokens - (p.slots[0] & 1);
+    }
+};
+__device__ __forceinline__ uint64_t tasks_of(const AppendParams& p) {
+    return ((uint64_t)p.tokens + (p.slots[0] & 1) + kTaskTokens - 1) / kTaskTokens * p.pool.heads;
 }
 
 template <int D>
 __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) {
     using C = Cell<D>;
-    constexpr uint32_t kLanes = D / 4;  // lanes of a row
+    constexpr int kG = C::kGroups;
+    const uint32_t lane = threadIdx.x & 31u, g = lane >> 2, q = lane & 3u;
     wait_for_previous();
-    const uint64_t rows = (uint64_t)p.tokens * p.pool.heads;
-    const uint64_t step = (uint64_t)gridDim.x * (kThreads / kLanes);
-    const uint32_t lr = threadIdx.x % kLanes, i = lr / 8, r = lr % 8;
-    for (uint64_t row0 = (uint64_t)blockIdx.x * (kThreads / kLanes); row0 < rows; row0 += step) {
-        const uint64_t row = row0 + threadIdx.x / kLanes;
-        uint32_t token = 0, h = 0, page = 0, off = 0;
-        bool live = row < rows;
-        if (live) {
-            token = (uint32_t)(row / p.pool.heads);
-            h = (uint32_t)(row % p.pool.heads);
-            live = locate(p.pool, p.slots[token], p.status, page, off);
-        }
-        uint32_t word[2], scale[2];
+    const uint64_t tasks = tasks_of(p);
+    for (uint64_t n = (uint64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32; n < tasks; n += (uint64_t)gridDim.x * (kThreads / 32)) {
+        const Task task(p, n);
+        const uint32_t h = task.h;
+        // ---- loads of both, then K: token g of the task ----
+        const int64_t token = task.token + g, va = task.token + 2 * q;
+        const Place at = locate<D>(p, token, h);
+        const Place place[2] = {locate<D>(p, va, h), locate<D>(p, va + 1, h)};
+        uint32_t xk[kG][8], xv[2][kG][4];
+        const uint16_t* row = p.rows[0] + token * p.token_stride[0] + (int64_t)h * p.head_stride[0] + 8 * q;
 #pragma unroll
-        for (int which = 0; which < 2; which++) {
-            uint32_t x[4] = {0, 0, 0, 0};
-            if (live)
-                load4(p.rows[which] + (int64_t)token * p.token_stride[which] + (int64_t)h * p.head_stride[which] + 4 * lr,
-                      p.vec, x);
-            word[which] = quantise4(x, scale[which]);
+        for (int i = 0; i < kG; i++) {
+#pragma unroll
+            for (int j = 0; j < 8; j++) xk[i][j] = 0;
+            if (at.cell) load_row<8>(row + 32 * i, p.vec, xk[i]);
         }
-        if (!live) continue;
-        uint16_t* cell = reinterpret_cast<uint16_t*>(p.pool.base + cell_offset<D>(p.pool, page, h, off));
-        const uint32_t t = off & 15u;
-        cell[C::k_word(t, i, r)] = (uint16_t)word[0];
-        cell[C::v_word(t, i, r)] = (uint16_t)word[1];
-        if (r == 0) {
-            cell[C::scale_word(t, i)] = (uint16_t)scale[0];
-            cell[C::scale_word(t, i) + D / 2] = (uint16_t)scale[1];
+#pragma unroll
+        for (int e = 0; e < 2; e++) {
+            const uint16_t* vrow = p.rows[1] + (va + e) * p.token_stride[1] + (int64_t)h * p.head_stride[1] + 4 * g;
+#pragma unroll
+            for (int i = 0; i < kG; i++) {
+#pragma unroll
+                for (int j = 0; j < 4; j++) xv[e][i][j] = 0;
+                if (place[e].cell) load_row<4>(vrow + 32 * i, p.vec, xv[e][i]);
+            }
         }
-        if (lr == 0) {
-            const uint64_t at = (((uint64_t)page * p.pool.heads + h) << p.pool.lg_page) + off;
-            if (p.weight) p.weight[at] = 0.f;
-            if (p.pos) p.pos[at] = p.positions[token];
+        uint32_t word[kG], scale[kG], both[kG];
+#pragma unroll
+        for (int i = 0; i < kG; i++) {
+            uint32_t top = largest(xk[i]);
+            top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+            top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+            scale[i] = scale_bits(top);
+            word[i] = codes_of<8>(xk[i], scale[i]);
+            // Word q of a pair's scales: this token's and its neighbour's.
+            both[i] = scale[i] | __shfl_xor_sync(0xFFFFFFFFu, scale[i], 4) << 16;
+        }
+        if (at.cell) {
+            put_words<kG>(at.cell + C::k_word(at.t, 0, 2 * q), word);
+            if (q == 0) {
+                if (p.weight) p.weight[at.entry] = 0.f;
+                if (p.pos) p.pos[at.entry] = p.positions[token];
+            }
+        }
+        // Scales: the even token's lane stores the pair's words.  Its two
+        // places are those of V's lane g / 2.
+        const int cell_pair = __shfl_sync(0xFFFFFFFFu, (int)side_by_side(place[0], place[1]), g >> 1);
+        if (q == 0 && at.cell) {
+            if (cell_pair) {
+                if (!(g & 1u)) put_words<kG>(at.cell + C::scale_word(at.t, 0), both);
+            } else {
+#pragma unroll
+                for (int i = 0; i < kG; i++) at.cell[C::scale_word(at.t, i)] = (uint16_t)scale[i];
+            }
+        }
+
+        // ---- V: tokens 2 q and 2 q + 1 ----
+        uint32_t code[2][kG], sv[2][kG];
+#pragma unroll
+        for (int e = 0; e < 2; e++)
+#pragma unroll
+            for (int i = 0; i < kG; i++) {
+                uint32_t top = largest(xv[e][i]);
+                top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 4));
+                top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 8));
+                top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16));
+                sv[e][i] = scale_bits(top);
+                code[e][i] = codes_of<4>(xv[e][i], sv[e][i]);
+            }
+        if (side_by_side(place[0], place[1])) {
+#pragma unroll
+            for (int i = 0; i < kG; i++) word[i] = code[0][i] | code[1][i] << 16, both[i] = sv[0][i] | sv[1][i] << 16;
+            put_words<kG>(place[0].cell + C::v_word(place[0].t, 0, g), word);
+            if (g == 0) put_words<kG>(place[0].cell + C::scale_word(place[0].t, 0) + D / 2, both);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+                if (!place[e].cell) continue;
+#pragma unroll
+                for (int i = 0; i < kG; i++) {
+                    place[e].cell[C::v_word(place[e].t, i, g)] = (uint16_t)code[e][i];
+                    if (g == 0) place[e].cell[C::scale_word(place[e].t, i) + D / 2] = (uint16_t)sv[e][i];
+                }
+            }
         }
     }
+}
+
+// Values of N codes.
+template <int N>
+__device__ __forceinline__ void values_of(uint32_t w, uint32_t scale, float (&v)[N]) {
+    const float s = bf16_float(scale);
+#pragma unroll
+    for (int j = 0; j < N; j++) v[j] = (float)((int)((w >> (4 * j)) & 15u) - 8) * s;
 }
 
 template <int D>
 __global__ void __launch_bounds__(kThreads) read_kernel(const AppendParams p) {
     using C = Cell<D>;
-    constexpr uint32_t kLanes = D / 4;
+    constexpr int kG = C::kGroups;
+    const uint32_t lane = threadIdx.x & 31u, g = lane >> 2, q = lane & 3u;
     wait_for_previous();
-    const uint64_t rows = (uint64_t)p.tokens * p.pool.heads;
-    const uint64_t step = (uint64_t)gridDim.x * (kThreads / kLanes);
-    const uint32_t lr = threadIdx.x % kLanes, i = lr / 8, r = lr % 8;
-    for (uint64_t row = (uint64_t)blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes; row < rows; row += step) {
-        const uint32_t token = (uint32_t)(row / p.pool.heads), h = (uint32_t)(row % p.pool.heads);
-        uint32_t page = 0, off = 0;
-        uint32_t word[2] = {0x8888u, 0x8888u}, scale[2] = {0, 0};
-        if (locate(p.pool, p.slots[token], p.status, page, off)) {
-            const uint16_t* cell =
-                reinterpret_cast<const uint16_t*>(p.pool.base + cell_offset<D>(p.pool, page, h, off));
-            const uint32_t t = off & 15u;
-            word[0] = cell[C::k_word(t, i, r)];
-            word[1] = cell[C::v_word(t, i, r)];
-            scale[0] = cell[C::scale_word(t, i)];
-            scale[1] = cell[C::scale_word(t, i) + D / 2];
+    const uint64_t tasks = tasks_of(p);
+    for (uint64_t n = (uint64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32; n < tasks; n += (uint64_t)gridDim.x * (kThreads / 32)) {
+        const Task task(p, n);
+        const uint32_t h = task.h;
+        const int64_t token = task.token + g, va = task.token + 2 * q;
+        const Place at = locate<D>(p, token, h);
+        const Place place[2] = {locate<D>(p, va, h), locate<D>(p, va + 1, h)};
+        uint32_t kw[kG], ks[kG], vw[2][kG], vs[2][kG];
+#pragma unroll
+        for (int i = 0; i < kG; i++) {
+            kw[i] = 0x88888888u, ks[i] = 0;
+            vw[0][i] = vw[1][i] = 0x8888u, vs[0][i] = vs[1][i] = 0;
+        }
+        if (at.cell) {
+            get_words<kG>(at.cell + C::k_word(at.t, 0, 2 * q), kw);
+            get_words<kG>(at.cell + C::scale_word(at.t & ~1u, 0), ks);  // of the pair
+#pragma unroll
+            for (int i = 0; i < kG; i++) ks[i] = at.t & 1u ? ks[i] >> 16 : ks[i] & 0xFFFFu;
+        }
+        const bool pair = side_by_side(place[0], place[1]);
+#pragma unroll
+        for (int e = 0; e < 2; e++) {
+            if (!place[e].cell || (pair && e)) continue;
+            uint32_t w[kG], s[kG];
+            const uint32_t even = place[e].t & ~1u;
+            get_words<kG>(place[e].cell + C::v_word(even, 0, g), w);
+            get_words<kG>(place[e].cell + C::scale_word(even, 0) + D / 2, s);
+#pragma unroll
+            for (int i = 0; i < kG; i++) {
+                vw[e][i] = place[e].t & 1u ? w[i] >> 16 : w[i] & 0xFFFFu;
+                vs[e][i] = place[e].t & 1u ? s[i] >> 16 : s[i] & 0xFFFFu;
+                if (pair) vw[1][i] = w[i] >> 16, vs[1][i] = s[i] >> 16;
+            }
+        }
+        if (token >= 0 && token < (int64_t)p.tokens) {
+            uint16_t* row = p.rows[0] + token * p.token_stride[0] + (int64_t)h * p.head_stride[0] + 8 * q;
+#pragma unroll
+            for (int i = 0; i < kG; i++) {
+                float v[8];
+                values_of<8>(kw[i], ks[i], v);
+                store_row<8>(row + 32 * i, p.vec, v);
+            }
         }
 #pragma unroll
-        for (int which = 0; which < 2; which++) {
-            uint16_t* out = p.rows[which] + (int64_t)token * p.token_stride[which] + (int64_t)h * p.head_stride[which] + 4 * lr;
-            float v[4];
+        for (int e = 0; e < 2; e++) {
+            if (va + e < 0 || va + e >= (int64_t)p.tokens) continue;
+            uint16_t* row = p.rows[1] + (va + e) * p.token_stride[1] + (int64_t)h * p.head_stride[1] + 4 * g;
 #pragma unroll
-            for (int j = 0; j < 4; j++)
-                v[j] = (float)((int)((word[which] >> (4 * j)) & 15u) - 8) * bf16_float(scale[which]);
-            if (p.vec) {
-                *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
-            } else {
-#pragma unroll
-                for (int j = 0; j < 4; j++) out[j] = (uint16_t)bf16_bits(v[j]);
+            for (int i = 0; i < kG; i++) {
+                float v[4];
+                values_of<4>(vw[e][i], vs[e][i], v);
+                store_row<4>(row + 32 * i, p.vec, v);
             }
         }
     }
@@ -150,8 +334,8 @@ cudaError_t launch(void (*kern)(AppendParams), const AppendParams& p, cudaStream
     int sms = 0, per_sm = 0;
     const cudaError_t err = kernel_fit(reinterpret_cast<const void*>(kern), kThreads, 0, &sms, &per_sm);
     if (err != cudaSuccess) return err;
-    const uint64_t per_block = kThreads / (p.pool.dim / 4);
-    const uint64_t need = ((uint64_t)p.tokens * p.pool.heads + per_block - 1) / per_block;
+    const uint64_t tasks = ((uint64_t)p.tokens + kTaskTokens) / kTaskTokens * p.pool.heads;
+    const uint64_t need = (tasks + kThreads / 32 - 1) / (kThreads / 32);
     const uint64_t fit = (uint64_t)sms * per_sm;
     return launch_dependent(kern, dim3((uint32_t)(need < fit ? need : fit)), dim3(kThreads), 0, s, p);
 }

@@ -48,7 +48,7 @@ struct AppendParams {
     float* weight;  // nullable
     int32_t* pos;   // nullable
     int* status;    // nullable
-    int vec;        // rows are 8-byte aligned
+    int vec;        // rows are 16-byte aligned
 };
 
 struct AttendParams {

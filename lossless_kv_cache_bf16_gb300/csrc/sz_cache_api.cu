@@ -77,7 +77,7 @@ bool rows_for(const void* d_k, int64_t k_token, int64_t k_head, const void* d_v,
     p->slots = d_slots;
     p->tokens = (uint32_t)tokens;
     p->status = d_status;
-    p->vec = aligned(d_k, 8) && aligned(d_v, 8) && multiple(k_token, k_head, 4) && multiple(v_token, v_head, 4);
+    p->vec = aligned(d_k, 16) && aligned(d_v, 16) && multiple(k_token, k_head, 8) && multiple(v_token, v_head, 8);
     return true;
 }
 
