@@ -5,8 +5,7 @@
 // corrected by its remainder, which fma gives exactly, so that
 // the codes are those of the definition: two bf16 significands have a
 // quotient that is k + 1/2 or at least 2^-17 away from it, which fp32 tells
-// apart.  |x / s| stays below 7.03, so that no code needs clamping, and the
-// sum of x / s and 1.5 * 2^23 + 8 holds the code in its low bits.
+// apart.  |x / s| stays below 7.03, so that no code needs clamping.
 //
 // Bound by memory: 4 D bytes of rows and 9 D / 8 of cache per token and head.
 // A warp takes 8 tokens of one head, and its lanes are laid out as the cell
@@ -26,23 +25,20 @@ namespace {
 constexpr uint32_t kThreads = 256;
 constexpr uint32_t kTaskTokens = 8;
 
-// N (4 or 8) bf16 bit patterns.
+// 2 N (4 or 8) bf16 values, two to a word.
 template <int N>
-__device__ __forceinline__ void load_row(const uint16_t* p, bool vec, uint32_t (&x)[N]) {
+__device__ __forceinline__ void load_row(const uint16_t* p, bool vec, uint32_t (&w)[N]) {
     if (vec) {
-        uint32_t w[N / 2];
-        if constexpr (N == 8) {
+        if constexpr (N == 4) {
             const uint4 v = *reinterpret_cast<const uint4*>(p);
             w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
         } else {
             const uint2 v = *reinterpret_cast<const uint2*>(p);
             w[0] = v.x, w[1] = v.y;
         }
-#pragma unroll
-        for (int j = 0; j < N / 2; j++) x[2 * j] = w[j] & 0xFFFFu, x[2 * j + 1] = w[j] >> 16;
     } else {
 #pragma unroll
-        for (int j = 0; j < N; j++) x[j] = p[j];
+        for (int j = 0; j < N; j++) w[j] = p[2 * j] | (uint32_t)p[2 * j + 1] << 16;
     }
 }
 
@@ -80,27 +76,39 @@ __device__ __forceinline__ uint32_t scale_bits(uint32_t top) {
     return top > 0x7F7Fu ? 0x7FC0u : s < 0x0080u ? 0u : s;
 }
 
-// Codes of N values, 4 bits each, x[0] lowest.
+// Codes of the 2 N values of w, 4 bits each, the first lowest.  The bits of
+// x / s + 1.5 * 2^23 + 8 are kMagic + code: they are added up as digits of 16,
+// and the sum of the kMagic taken off at the end.
 template <int N>
-__device__ __forceinline__ uint32_t codes_of(const uint32_t (&x)[N], uint32_t scale) {
+__device__ __forceinline__ uint32_t codes_of(const uint32_t (&w)[N], uint32_t scale) {
+    constexpr uint32_t kMagic = 0x4B400000u;
+    constexpr uint32_t kSum = N == 4 ? kMagic * 0x11111111u : kMagic * 0x1111u;
     const bool usable = scale - 1u < 0x7F7Fu;  // neither 0 nor a NaN
     const float s = usable ? bf16_float(scale) : 1.f, inv = reciprocal(s);
-    uint32_t w = 0;
+    uint32_t sum = 0;
 #pragma unroll
     for (int j = N - 1; j >= 0; j--) {
-        const float q = quotient(bf16_float(x[j]), s, inv);
-        w = (w << 4) | (__float_as_uint(q + 12582920.f) & 15u);
+        sum = sum * 16u + __float_as_uint(quotient(__uint_as_float(w[j] & 0xFFFF0000u), s, inv) + 12582920.f);
+        sum = sum * 16u + __float_as_uint(quotient(__uint_as_float(w[j] << 16), s, inv) + 12582920.f);
     }
-    return usable ? w : 0x88888888u >> (32 - 4 * N);
+    return usable ? sum - kSum : 0x88888888u >> (32 - 8 * N);
 }
 
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+// The largest |x| of w, as bf16 bits (which compare like the value), in the
+// larger of the result's halves.
 template <int N>
-__device__ __forceinline__ uint32_t largest(const uint32_t (&x)[N]) {
-    uint32_t top = 0;  // |x| as bf16 bits compares like the value
+__device__ __forceinline__ uint32_t largest(const uint32_t (&w)[N]) {
+    uint32_t top = w[0] & 0x7FFF7FFFu;
 #pragma unroll
-    for (int j = 0; j < N; j++) top = max(top, x[j] & 0x7FFFu);
+    for (int j = 1; j < N; j++) top = max_u16x2(top, w[j] & 0x7FFF7FFFu);
     return top;
 }
+__device__ __forceinline__ uint32_t larger_half(uint32_t x) { return max(x & 0xFFFFu, x >> 16); }
 
 // A token's place: its cell (null where the token is left out: slot -1, or one
 // outside the pool, which is reported) and its number in the cell.
@@ -179,13 +187,13 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) 
         const int64_t token = task.token + g, va = task.token + 2 * q;
         const Place at = locate<D>(p, token, h);
         const Place place[2] = {locate<D>(p, va, h), locate<D>(p, va + 1, h)};
-        uint32_t xk[kG][8], xv[2][kG][4];
+        uint32_t xk[kG][4], xv[2][kG][2];
         const uint16_t* row = p.rows[0] + token * p.token_stride[0] + (int64_t)h * p.head_stride[0] + 8 * q;
 #pragma unroll
         for (int i = 0; i < kG; i++) {
 #pragma unroll
-            for (int j = 0; j < 8; j++) xk[i][j] = 0;
-            if (at.cell) load_row<8>(row + 32 * i, p.vec, xk[i]);
+            for (int j = 0; j < 4; j++) xk[i][j] = 0;
+            if (at.cell) load_row<4>(row + 32 * i, p.vec, xk[i]);
         }
 #pragma unroll
         for (int e = 0; e < 2; e++) {
@@ -193,18 +201,18 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) 
 #pragma unroll
             for (int i = 0; i < kG; i++) {
 #pragma unroll
-                for (int j = 0; j < 4; j++) xv[e][i][j] = 0;
-                if (place[e].cell) load_row<4>(vrow + 32 * i, p.vec, xv[e][i]);
+                for (int j = 0; j < 2; j++) xv[e][i][j] = 0;
+                if (place[e].cell) load_row<2>(vrow + 32 * i, p.vec, xv[e][i]);
             }
         }
         uint32_t word[kG], scale[kG], both[kG];
 #pragma unroll
         for (int i = 0; i < kG; i++) {
             uint32_t top = largest(xk[i]);
-            top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-            top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-            scale[i] = scale_bits(top);
-            word[i] = codes_of<8>(xk[i], scale[i]);
+            top = max_u16x2(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+            top = max_u16x2(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+            scale[i] = scale_bits(larger_half(top));
+            word[i] = codes_of<4>(xk[i], scale[i]);
             // Word q of a pair's scales: this token's and its neighbour's.
             both[i] = scale[i] | __shfl_xor_sync(0xFFFFFFFFu, scale[i], 4) << 16;
         }
@@ -234,11 +242,11 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) 
 #pragma unroll
             for (int i = 0; i < kG; i++) {
                 uint32_t top = largest(xv[e][i]);
-                top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 4));
-                top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 8));
-                top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16));
-                sv[e][i] = scale_bits(top);
-                code[e][i] = codes_of<4>(xv[e][i], sv[e][i]);
+                top = max_u16x2(top, __shfl_xor_sync(0xFFFFFFFFu, top, 4));
+                top = max_u16x2(top, __shfl_xor_sync(0xFFFFFFFFu, top, 8));
+                top = max_u16x2(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16));
+                sv[e][i] = scale_bits(larger_half(top));
+                code[e][i] = codes_of<2>(xv[e][i], sv[e][i]);
             }
         if (side_by_side(place[0], place[1])) {
 #pragma unroll
