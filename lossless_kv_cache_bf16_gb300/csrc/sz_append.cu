@@ -108,7 +108,10 @@ __device__ __forceinline__ uint32_t largest(const uint32_t (&w)[N]) {
     for (int j = 1; j < N; j++) top = max_u16x2(top, w[j] & 0x7FFF7FFFu);
     return top;
 }
-__device__ __forceinline__ uint32_t larger_half(uint32_t x) { return max(x & 0xFFFFu, x >> 16); }
+// The larger halves of a and of b, in the low and the high half.
+__device__ __forceinline__ uint32_t larger_halves(uint32_t a, uint32_t b) {
+    return max_u16x2(prmt(a, b, 0x5410u), prmt(a, b, 0x7632u));
+}
 
 // A token's place: its cell (null where the token is left out: slot -1, or one
 // outside the pool, which is reported) and its number in the cell.
@@ -132,6 +135,15 @@ __device__ __forceinline__ Place locate(const AppendParams& p, int64_t token, ui
     at.t = off & 15u;
     at.entry = (((uint64_t)page * p.pool.heads + h) << p.pool.lg_page) + off;
     return at;
+}
+
+// Another lane's cell and token number.
+__device__ __forceinline__ Place from_lane(const Place& a, uint32_t lane) {
+    Place b;
+    b.cell = reinterpret_cast<uint16_t*>(__shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(a.cell), lane));
+    b.t = __shfl_sync(0xFFFFFFFFu, a.t, lane);
+    b.entry = 0;
+    return b;
 }
 
 // Whether two tokens' words lie side by side.
@@ -186,7 +198,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) 
         // ---- loads of both, then K: token g of the task ----
         const int64_t token = task.token + g, va = task.token + 2 * q;
         const Place at = locate<D>(p, token, h);
-        const Place place[2] = {locate<D>(p, va, h), locate<D>(p, va + 1, h)};
+        const Place place[2] = {from_lane(at, 8 * q), from_lane(at, 8 * q + 4)};  // of tokens 2 q and 2 q + 1
         uint32_t xk[kG][4], xv[2][kG][2];
         const uint16_t* row = p.rows[0] + token * p.token_stride[0] + (int64_t)h * p.head_stride[0] + 8 * q;
 #pragma unroll
@@ -205,13 +217,18 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) 
                 if (place[e].cell) load_row<2>(vrow + 32 * i, p.vec, xv[e][i]);
             }
         }
+        // Two groups' maxima share a word while the lanes of a group compare theirs.
         uint32_t word[kG], scale[kG], both[kG];
 #pragma unroll
-        for (int i = 0; i < kG; i++) {
-            uint32_t top = largest(xk[i]);
+        for (int i = 0; i < kG; i += 2) {
+            uint32_t top = larger_halves(largest(xk[i]), largest(xk[i + 1]));
             top = max_u16x2(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
             top = max_u16x2(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-            scale[i] = scale_bits(larger_half(top));
+            scale[i] = scale_bits(top & 0xFFFFu);
+            scale[i + 1] = scale_bits(top >> 16);
+        }
+#pragma unroll
+        for (int i = 0; i < kG; i++) {
             word[i] = codes_of<4>(xk[i], scale[i]);
             // Word q of a pair's scales: this token's and its neighbour's.
             both[i] = scale[i] | __shfl_xor_sync(0xFFFFFFFFu, scale[i], 4) << 16;
@@ -238,16 +255,16 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) 
         // ---- V: tokens 2 q and 2 q + 1 ----
         uint32_t code[2][kG], sv[2][kG];
 #pragma unroll
-        for (int e = 0; e < 2; e++)
+        for (int i = 0; i < kG; i++) {
+            uint32_t top = larger_halves(largest(xv[0][i]), largest(xv[1][i]));
+            top = max_u16x2(top, __shfl_xor_sync(0xFFFFFFFFu, top, 4));
+            top = max_u16x2(top, __shfl_xor_sync(0xFFFFFFFFu, top, 8));
+            top = max_u16x2(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16));
+            sv[0][i] = scale_bits(top & 0xFFFFu);
+            sv[1][i] = scale_bits(top >> 16);
 #pragma unroll
-            for (int i = 0; i < kG; i++) {
-                uint32_t top = largest(xv[e][i]);
-                top = max_u16x2(top, __shfl_xor_sync(0xFFFFFFFFu, top, 4));
-                top = max_u16x2(top, __shfl_xor_sync(0xFFFFFFFFu, top, 8));
-                top = max_u16x2(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16));
-                sv[e][i] = scale_bits(larger_half(top));
-                code[e][i] = codes_of<2>(xv[e][i], sv[e][i]);
-            }
+            for (int e = 0; e < 2; e++) code[e][i] = codes_of<2>(xv[e][i], sv[e][i]);
+        }
         if (side_by_side(place[0], place[1])) {
 #pragma unroll
             for (int i = 0; i < kG; i++) word[i] = code[0][i] | code[1][i] << 16, both[i] = sv[0][i] | sv[1][i] << 16;
@@ -287,7 +304,7 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const AppendParams p) {
         const uint32_t h = task.h;
         const int64_t token = task.token + g, va = task.token + 2 * q;
         const Place at = locate<D>(p, token, h);
-        const Place place[2] = {locate<D>(p, va, h), locate<D>(p, va + 1, h)};
+        const Place place[2] = {from_lane(at, 8 * q), from_lane(at, 8 * q + 4)};  // of tokens 2 q and 2 q + 1
         uint32_t kw[kG], ks[kG], vw[2][kG], vs[2][kG];
 #pragma unroll
         for (int i = 0; i < kG; i++) {
