@@ -26,7 +26,7 @@ namespace {
 
 constexpr uint32_t kThreads = 256;
 constexpr uint32_t kMaxRot = 256;
-constexpr uint32_t kMaxTile = 4;  // tokens of a block at a time
+constexpr uint32_t kMaxTile = 16;  // tokens of a block at a time
 
 template <bool VEC>
 __device__ __forceinline__ void load8(const uint16_t* p, float (&x)[8]) {
@@ -190,10 +190,11 @@ cudaError_t launch(const NormRopeParams& p, cudaStream_t s) {
     int sms = 0, per_sm = 0;
     const cudaError_t err = kernel_fit(reinterpret_cast<const void*>(norm_rope_kernel<D, VEC>), kThreads, 0, &sms, &per_sm);
     if (err != cudaSuccess) return err;
-    // Several tokens at a time fill the block's threads; with few tokens, a
-    // block for each is done sooner.
+    // As many tokens at a time as leave every block the same number of times:
+    // one token each while there are fewer tokens than blocks.
     const uint32_t fit = (uint32_t)sms * per_sm;
-    const uint32_t tile = p.tokens >= kMaxTile * fit ? kMaxTile : p.tokens >= 2 * fit ? 2u : 1u;
+    const uint32_t times = (p.tokens + kMaxTile * fit - 1) / (kMaxTile * fit);
+    const uint32_t tile = (p.tokens + times * fit - 1) / (times * fit);
     const uint32_t need = (p.tokens + tile - 1) / tile;
     return launch_dependent(norm_rope_kernel<D, VEC>, dim3(need < fit ? need : fit), dim3(kThreads), 0, s, p, tile);
 }
