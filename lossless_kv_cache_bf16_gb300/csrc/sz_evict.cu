@@ -9,11 +9,14 @@
 // travel with them.  Sources and targets are disjoint, so the moves need no
 // order among themselves.
 //
-// First kernel, one block per (sequence, kv head): weights as 32-bit keys
-// whose unsigned order is theirs, a radix selection of the keep-th largest
-// (11, 11 and 10 bits), then three passes in slot order over contiguous runs
-// of slots, one per warp: ties that survive, holes and movers are counted,
-// then numbered.  Second kernel: the moves, one warp each.
+// First kernel, one cluster of blocks per (sequence, kv head): weights as
+// 32-bit keys whose unsigned order is theirs, held in registers (warp after
+// warp takes a contiguous run of slots), a radix selection of the keep-th
+// largest (11, 11 and 10 bits), then three passes in slot order: ties that
+// survive, holes and movers are counted, then numbered.  The blocks of a
+// cluster join their histograms and counts through each other's shared
+// memory.  Second kernel: the moves, four at a time to a warp.  Both are
+// bound by latency: 8 bytes a slot are read, and few tokens move.
 #include "sz_cache.cuh"
 #include "sz_params.h"
 
@@ -22,9 +25,32 @@ namespace {
 
 constexpr uint32_t kThreads = 1024;
 constexpr uint32_t kWarps = kThreads / 32;
-constexpr uint32_t kKeysShared = 51200;  // keys that fit in shared memory; longer sequences read theirs again per pass
+constexpr uint32_t kMaxCluster = 8;
 constexpr uint32_t kBins = 2048;
+constexpr uint32_t kCopies = 4;  // of the first histogram: keys of neighbouring lanes often share a bin
 constexpr uint32_t kProtected = 0xFFFFFFFFu;
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+// All threads of the cluster; shared memory written before is seen after.
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// A word of this block's shared memory as block `rank` of the cluster holds it.
+__device__ __forceinline__ uint32_t peer_word(const uint32_t* p, uint32_t rank) {
+    uint32_t a, v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
 
 // Unsigned order of the key = order of the weight; NaN counts as -infinity,
 // -0 as 0.  At most 0xFF800000 (+infinity), so protected tokens come first.
@@ -56,55 +82,99 @@ struct Slots {
     }
 };
 
-// Sums of the counts of the warps before this one.
-__device__ __forceinline__ void warp_offsets(uint32_t (*s_count)[3], uint32_t warp, uint32_t (&off)[3]) {
-#pragma unroll
-    for (int k = 0; k < 3; k++) off[k] = 0;
-    for (uint32_t w = 0; w < warp; w++)
-#pragma unroll
-        for (int k = 0; k < 3; k++) off[k] += s_count[w][k];
-}
-
-__global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictParams p, const uint32_t shared_keys) {
-    extern __shared__ uint32_t s_keys[];
-    __shared__ uint32_t s_bins[kBins];
-    __shared__ uint32_t s_count[kWarps][3];
+// KEYS: keys that a thread holds, 32 * KEYS to a warp; 0: more than fit, read
+// again for every pass.
+template <int KEYS>
+__global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictParams p) {
+    __shared__ uint32_t s_bins[kCopies * kBins];
+    __shared__ uint32_t s_total[kBins];
+    __shared__ uint32_t s_count[kWarps];
+    __shared__ uint32_t s_sum[4];  // of the block: protected, ties, holes, movers
     __shared__ uint32_t s_pick[2];
     wait_for_previous();
     const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31u;
-    const Slots slots{p, blockIdx.y, blockIdx.x};
-    const uint32_t list = blockIdx.y * p.pool.heads + blockIdx.x;
+    const uint32_t rank = cluster_rank(), blocks = cluster_size();
+    const Slots slots{p, blockIdx.z, blockIdx.y};
+    const uint32_t list = blockIdx.z * p.pool.heads + blockIdx.y;
     const int32_t len = p.lens[slots.b];
     const bool ok = len >= 0 && (uint64_t)len <= (uint64_t)p.table_width << p.pool.lg_page;
     const uint32_t n = ok ? (uint32_t)len : 0u;
-    if (tid == 0) {
+    if (tid == 0 && rank == 0) {
         if (!ok && p.status) atomicMax(p.status, kStatusInvalid);
-        if (blockIdx.x == 0) p.new_lens[slots.b] = (int32_t)min(n, p.keep);
+        if (blockIdx.y == 0) p.new_lens[slots.b] = (int32_t)min(n, p.keep);
         if (n <= p.keep) p.moves[list] = 0;
     }
-    if (n <= p.keep) return;
+    if (n <= p.keep) return;  // the whole cluster
     const int64_t safe_from = (int64_t)p.next_pos[slots.b] - (int64_t)p.recent;
-    const bool cached = n <= shared_keys;
+
+    // This warp's slots [from, to), in order of block and warp.
+    const uint32_t runs = blocks * kWarps;
+    const uint32_t run = ((n + runs - 1) / runs + 31u) & ~31u;
+    const uint64_t first = (uint64_t)(rank * kWarps + warp) * run;
+    const uint32_t from = (uint32_t)min(first, (uint64_t)n), to = (uint32_t)min(first + run, (uint64_t)n);
+    uint32_t keys[KEYS ? KEYS : 1];
+    bool only_safe = false;
+    auto load_keys = [&]() {
+        if constexpr (KEYS > 0) {
+#pragma unroll
+            for (int j = 0; j < KEYS; j++) {
+                const uint32_t i = from + 32 * j + lane;
+                keys[j] = i < to ? slots.key(i, safe_from, only_safe) : 0u;
+            }
+        }
+    };
+    // Calls f(slot, key, whether there is such a slot) for the warp's slots in
+    // order, 32 at a time, by whole warps.
+    auto each = [&](auto f) {
+        if constexpr (KEYS > 0) {
+#pragma unroll
+            for (int j = 0; j < KEYS; j++) {
+                const uint32_t i0 = from + 32 * j;
+                if (i0 < to) f(i0 + lane, keys[j], i0 + lane < to);
+            }
+        } else {
+            for (uint32_t i0 = from; i0 < to; i0 += 32) {
+                const bool in = i0 + lane < to;
+                f(i0 + lane, in ? slots.key(i0 + lane, safe_from, only_safe) : 0u, in);
+            }
+        }
+    };
+    // Sum over the block's warps of x (one value per warp), in s_sum[k], and
+    // what the warps and blocks before this warp have.
+    auto place = [&](uint32_t x, int k, uint32_t& all) {
+        if (lane == 0) s_count[warp] = x;
+        __syncthreads();
+        if (warp == 0) {
+            uint32_t upto = s_count[lane];
+#pragma unroll
+            for (int d = 1; d < 32; d *= 2) {
+                const uint32_t o = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+                if (lane >= (uint32_t)d) upto += o;
+            }
+            s_count[lane] = upto;
+            if (lane == 31) s_sum[k] = upto;
+        }
+        cluster_sync();
+        uint32_t before = warp ? s_count[warp - 1] : 0u;
+        all = 0;
+        for (uint32_t r = 0; r < blocks; r++) {
+            const uint32_t v = peer_word(&s_sum[k], r);
+            all += v;
+            if (r < rank) before += v;
+        }
+        __syncthreads();  // s_count is written again by the next call
+        return before;
+    };
 
     // ---- keys, and the protected ones' number ----
-    uint32_t safe = 0;
-    for (uint32_t i = tid; i < n; i += kThreads) {
-        const uint32_t k = slots.key(i, safe_from, false);
-        if (cached) s_keys[i] = k;
-        safe += k == kProtected;
+    load_keys();
+    uint32_t mine = 0, safe = 0;
+    each([&](uint32_t, uint32_t k, bool in) { mine += __popc(__ballot_sync(0xFFFFFFFFu, in && k == kProtected)); });
+    place(mine, 0, safe);
+    if (safe >= p.keep) {
+        only_safe = true;
+        load_keys();
     }
-    safe = __reduce_add_sync(0xFFFFFFFFu, safe);
-    if (lane == 0) s_count[warp][0] = safe;
-    __syncthreads();
-    safe = 0;
-    for (uint32_t w = 0; w < kWarps; w++) safe += s_count[w][0];
-    const bool only_safe = safe >= p.keep;
-    if (only_safe && cached) {
-        __syncthreads();
-        for (uint32_t i = tid; i < n; i += kThreads) s_keys[i] = slots.key(i, safe_from, true);
-        __syncthreads();
-    }
-    auto key = [&](uint32_t i) { return cached ? s_keys[i] : slots.key(i, safe_from, only_safe); };
 
     // ---- the threshold: `need` of the tokens whose key equals it survive ----
     const uint32_t apart = only_safe ? 0u : kProtected;  // keys that do not compete
@@ -112,32 +182,46 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictParam
     uint32_t fixed = 0;  // mask of the bits chosen so far
     for (int level = 0; level < 3; level++) {
         const int shift = level == 0 ? 21 : level == 1 ? 10 : 0;
-        const uint32_t width = level == 2 ? 1024 : 2048;
-        for (uint32_t i = tid; i < kBins; i += kThreads) s_bins[i] = 0;
+        const uint32_t width = level == 2 ? 1024 : 2048, copies = level == 0 ? kCopies : 1;
+        for (uint32_t i = tid; i < copies * kBins; i += kThreads) s_bins[i] = 0;
         __syncthreads();
-        for (uint32_t i0 = warp * 32; i0 < n; i0 += kThreads) {
-            const uint32_t i = i0 + lane;
-            const uint32_t k = i < n ? key(i) : apart;
-            const bool in = k != apart && (k & fixed) == threshold;
+        uint32_t* bins = s_bins + (level == 0 ? lane % kCopies * kBins : 0);
+        each([&](uint32_t, uint32_t k, bool in) {
+            in = in && k != apart && (k & fixed) == threshold;
             const uint32_t bin = (k >> shift) & (width - 1);
             const uint32_t who = __ballot_sync(0xFFFFFFFFu, in);
-            if (!who) continue;
+            if (!who) return;
             // A warp whose keys share a bin (equal weights) adds once.
             const uint32_t lead = __ffs(who) - 1;
             const uint32_t bin0 = __shfl_sync(0xFFFFFFFFu, bin, lead);
             if (__all_sync(0xFFFFFFFFu, !in || bin == bin0)) {
                 if (lane == lead) atomicAdd(&s_bins[bin0], __popc(who));
             } else if (in) {
-                atomicAdd(&s_bins[bin], 1u);
+                atomicAdd(&bins[bin], 1u);
+            }
+        });
+        __syncthreads();
+        if (level == 0) {
+            for (uint32_t i = tid; i < kBins; i += kThreads) {
+                uint32_t sum = 0;
+                for (uint32_t c = 0; c < kCopies; c++) sum += s_bins[c * kBins + i];
+                s_bins[i] = sum;
             }
         }
-        __syncthreads();
+        cluster_sync();
+        for (uint32_t i = tid; i < width; i += kThreads) {
+            uint32_t sum = 0;
+            for (uint32_t r = 0; r < blocks; r++) sum += peer_word(&s_bins[i], r);
+            s_total[i] = sum;
+        }
+        // No block clears its bins while another reads them.
+        cluster_sync();
         // Warp 0 finds the bin that holds the need-th largest: each lane sums
         // a run of bins, top lane first.
         if (warp == 0) {
             const uint32_t per = width / 32, hi = width - lane * per;
             uint32_t sum = 0;
-            for (uint32_t j = 1; j <= per; j++) sum += s_bins[hi - j];
+            for (uint32_t j = 1; j <= per; j++) sum += s_total[hi - j];
             uint32_t upto = sum;
 #pragma unroll
             for (int d = 1; d < 32; d *= 2) {
@@ -147,7 +231,7 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictParam
             const uint32_t past = __ballot_sync(0xFFFFFFFFu, upto >= need);
             if (past && lane == (uint32_t)(__ffs(past) - 1)) {
                 uint32_t left = need - (upto - sum), j = 1;
-                while (j < per && s_bins[hi - j] < left) left -= s_bins[hi - j], j++;
+                while (j < per && s_total[hi - j] < left) left -= s_total[hi - j], j++;
                 s_pick[0] = hi - j;
                 s_pick[1] = left;
             }
@@ -159,51 +243,38 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictParam
     }
 
     // ---- survivors, holes and movers, in slot order ----
-    const uint32_t run = ((n + kWarps - 1) / kWarps + 31u) & ~31u;
-    const uint32_t from = min(warp * run, n), to = min(from + run, n);
-    uint32_t ties = 0;
-    for (uint32_t i0 = from; i0 < to; i0 += 32)
-        ties += __popc(__ballot_sync(0xFFFFFFFFu, i0 + lane < to && key(i0 + lane) == threshold));
-    if (lane == 0) s_count[warp][0] = ties, s_count[warp][1] = 0, s_count[warp][2] = 0;
-    __syncthreads();
-    uint32_t off[3];
-    warp_offsets(s_count, warp, off);
-    const uint32_t ties_before = off[0];
-    __syncthreads();
+    const uint32_t below = (1u << lane) - 1u;
+    uint32_t ties = 0, all = 0;
+    each([&](uint32_t, uint32_t k, bool in) { ties += __popc(__ballot_sync(0xFFFFFFFFu, in && k == threshold)); });
+    const uint32_t ties_before = place(ties, 1, all);
+    // Calls f(slot, holes, movers) for the warp's slots, with the ballots.
+    auto sort_out = [&](auto f) {
+        uint32_t tie = ties_before;
+        each([&](uint32_t i, uint32_t k, bool in) {
+            const uint32_t eq = __ballot_sync(0xFFFFFFFFu, in && k == threshold);
+            const bool stays = in && (k > threshold || (k == threshold && tie + __popc(eq & below) < need));
+            tie += __popc(eq);
+            f(i, __ballot_sync(0xFFFFFFFFu, in && i < p.keep && !stays), __ballot_sync(0xFFFFFFFFu, i >= p.keep && stays));
+        });
+    };
+    uint32_t holes = 0, movers = 0;
+    sort_out([&](uint32_t, uint32_t hb, uint32_t mb) { holes += __popc(hb), movers += __popc(mb); });
+    uint32_t hole = place(holes, 2, all);
+    if (tid == 0 && rank == 0) p.moves[list] = min(all, p.max_moves);
+    uint32_t mover = place(movers, 3, all);
     uint32_t* to_list = p.pairs + 2ull * list * p.max_moves;
     uint32_t* from_list = to_list + p.max_moves;
-    uint32_t holes = 0, movers = 0;
-    const uint32_t below = (1u << lane) - 1u;
-    for (int write = 0; write < 2; write++) {
-        uint32_t tie = ties_before, hole = holes, mover = movers;
-        for (uint32_t i0 = from; i0 < to; i0 += 32) {
-            const uint32_t i = i0 + lane;
-            const uint32_t k = i < to ? key(i) : 0u;
-            const uint32_t eq = __ballot_sync(0xFFFFFFFFu, i < to && k == threshold);
-            const bool stays = i < to && (k > threshold || (k == threshold && tie + __popc(eq & below) < need));
-            tie += __popc(eq);
-            const uint32_t hb = __ballot_sync(0xFFFFFFFFu, i < to && i < p.keep && !stays);
-            const uint32_t mb = __ballot_sync(0xFFFFFFFFu, i >= p.keep && stays);
-            if (write) {
-                const uint32_t hi = hole + __popc(hb & below), mi = mover + __popc(mb & below);
-                if (hb >> lane & 1u && hi < p.max_moves) to_list[hi] = i;
-                if (mb >> lane & 1u && mi < p.max_moves) from_list[mi] = i;
-            }
-            hole += __popc(hb);
-            mover += __popc(mb);
-        }
-        if (write) break;
-        if (lane == 0) s_count[warp][1] = hole, s_count[warp][2] = mover;
-        __syncthreads();
-        warp_offsets(s_count, warp, off);
-        holes = off[1], movers = off[2];
-        if (tid == 0) {
-            uint32_t all = 0;
-            for (uint32_t w = 0; w < kWarps; w++) all += s_count[w][1];
-            p.moves[list] = min(all, p.max_moves);
-        }
-    }
+    sort_out([&](uint32_t i, uint32_t hb, uint32_t mb) {
+        const uint32_t hi = hole + __popc(hb & below), mi = mover + __popc(mb & below);
+        if (hb >> lane & 1u && hi < p.max_moves) to_list[hi] = i;
+        if (mb >> lane & 1u && mi < p.max_moves) from_list[mi] = i;
+        hole += __popc(hb);
+        mover += __popc(mb);
+    });
+    cluster_sync();  // no block leaves while another reads its counts
 }
+
+constexpr uint32_t kTogether = 4;  // moves of a warp at a time
 
 template <int D>
 __global__ void __launch_bounds__(256) evict_move_kernel(const EvictParams p) {
@@ -214,49 +285,94 @@ __global__ void __launch_bounds__(256) evict_move_kernel(const EvictParams p) {
     const uint32_t list = blockIdx.z * p.pool.heads + blockIdx.y;
     const uint32_t n = p.moves[list];
     const uint32_t* to_list = p.pairs + 2ull * list * p.max_moves;
-    for (uint32_t k = blockIdx.x * 8 + threadIdx.x / 32; k < n; k += gridDim.x * 8) {
-        const uint32_t slot[2] = {to_list[k], to_list[p.max_moves + k]};
-        uint64_t at[2];
-        if (!slots.find(slot[0], at[0]) || !slots.find(slot[1], at[1])) continue;
-        uint16_t* cell[2];
-        uint32_t tok[2];
+    // Lane l: K and V word l (of D / 4), and a scale word in the first D / 16 lanes.
+    const uint32_t i = lane / 8, r = lane % 8, j = lane % (D / 32);
+    const uint32_t value = lane < D / 32 ? 0 : D / 2;
+    for (uint32_t k0 = (blockIdx.x * 8 + threadIdx.x / 32) * kTogether; k0 < n; k0 += gridDim.x * 8 * kTogether) {
+        // Entry of the tables, target in lanes 0 .. 3 and source in lanes 4 .. 7.
+        uint64_t at = 0;
+        bool good = false;
+        if (lane < 2 * kTogether && k0 + lane % kTogether < n)
+            good = slots.find(to_list[(lane < kTogether ? 0 : p.max_moves) + k0 + lane % kTogether], at);
+        const uint32_t mask = __ballot_sync(0xFFFFFFFFu, good);
+        uint16_t v[kTogether][3];
+        uint16_t* target[kTogether];
+        uint32_t tok[kTogether];
+        float weight[kTogether];
+        int32_t pos[kTogether];
+        uint64_t entry[kTogether];
 #pragma unroll
-        for (int e = 0; e < 2; e++) {
-            cell[e] = reinterpret_cast<uint16_t*>(p.pool.base + (at[e] >> 4) * C::kBytes);
-            tok[e] = (uint32_t)at[e] & 15u;
+        for (uint32_t e = 0; e < kTogether; e++) {
+            entry[e] = __shfl_sync(0xFFFFFFFFu, at, e);
+            const uint64_t from = __shfl_sync(0xFFFFFFFFu, at, kTogether + e);
+            target[e] = nullptr;
+            if ((mask >> e & mask >> (kTogether + e) & 1u) == 0) continue;
+            target[e] = reinterpret_cast<uint16_t*>(p.pool.base + (entry[e] >> 4) * C::kBytes);
+            tok[e] = (uint32_t)entry[e] & 15u;
+            const uint16_t* cell = reinterpret_cast<const uint16_t*>(p.pool.base + (from >> 4) * C::kBytes);
+            const uint32_t t = (uint32_t)from & 15u;
+            if (lane < D / 4) {
+                v[e][0] = cell[C::k_word(t, i, r)];
+                v[e][1] = cell[C::v_word(t, i, r)];
+            }
+            if (lane < D / 16) v[e][2] = cell[C::scale_word(t, j) + value];
+            if (lane == 0) weight[e] = p.weight[from];
+            if (lane == 1) pos[e] = p.pos[from];
         }
-        // Lane l: K and V word l (of D / 4), and a scale word in the first D / 16 lanes.
-        uint16_t v[3];
-        const uint32_t i = lane / 8, r = lane % 8, j = lane % (D / 32);
-        if (lane < D / 4) {
-            v[0] = cell[1][C::k_word(tok[1], i, r)];
-            v[1] = cell[1][C::v_word(tok[1], i, r)];
+#pragma unroll
+        for (uint32_t e = 0; e < kTogether; e++) {
+            if (!target[e]) continue;
+            if (lane < D / 4) {
+                target[e][C::k_word(tok[e], i, r)] = v[e][0];
+                target[e][C::v_word(tok[e], i, r)] = v[e][1];
+            }
+            if (lane < D / 16) target[e][C::scale_word(tok[e], j) + value] = v[e][2];
+            if (lane == 0) p.weight[entry[e]] = weight[e];
+            if (lane == 1) p.pos[entry[e]] = pos[e];
         }
-        if (lane < D / 16) v[2] = cell[1][C::scale_word(tok[1], j) + (lane < D / 32 ? 0 : D / 2)];
-        if (lane < D / 4) {
-            cell[0][C::k_word(tok[0], i, r)] = v[0];
-            cell[0][C::v_word(tok[0], i, r)] = v[1];
-        }
-        if (lane < D / 16) cell[0][C::scale_word(tok[0], j) + (lane < D / 32 ? 0 : D / 2)] = v[2];
-        if (lane == 0) p.weight[at[0]] = p.weight[at[1]];
-        if (lane == 1) p.pos[at[0]] = p.pos[at[1]];
     }
+}
+
+cudaError_t launch_select(void (*kern)(EvictParams), const EvictParams& p, uint32_t cluster, cudaStream_t s) {
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {cluster, 1, 1};
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(cluster, p.pool.heads, p.batch);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
 }  // namespace
 
 cudaError_t launch_evict(const EvictParams& p, cudaStream_t s) {
     int sms = 0, per_sm = 0;
-    const size_t smem = 4ull * kKeysShared;
-    cudaError_t err = kernel_fit(reinterpret_cast<const void*>(evict_select_kernel), kThreads, smem, &sms, &per_sm);
+    cudaError_t err = kernel_fit(reinterpret_cast<const void*>(evict_select_kernel<0>), kThreads, 0, &sms, &per_sm);
     if (err != cudaSuccess) return err;
-    const uint64_t longest = (uint64_t)p.table_width << p.pool.lg_page;
-    const size_t take = longest < kKeysShared ? 4 * longest : smem;
-    err = launch_dependent(evict_select_kernel, dim3(p.pool.heads, p.batch), dim3(kThreads), take, s, p, (uint32_t)(take / 4));
+    // As many blocks a list as fit on the device at once, and at least as many
+    // as hold the longest sequence's keys, 32 a thread (beyond 8 blocks the
+    // keys are read again for every pass).
+    const uint64_t lists = (uint64_t)p.pool.heads * p.batch, longest = (uint64_t)p.table_width << p.pool.lg_page;
+    uint32_t cluster = 1;
+    while (cluster < kMaxCluster && longest > (uint64_t)cluster * kThreads &&
+           (lists * cluster * 2 <= (uint64_t)sms || longest > 32ull * cluster * kThreads))
+        cluster *= 2;
+    const uint64_t keys = (longest + (uint64_t)cluster * kThreads - 1) / ((uint64_t)cluster * kThreads);
+    err = launch_select(keys <= 2    ? evict_select_kernel<2>
+                        : keys <= 8  ? evict_select_kernel<8>
+                        : keys <= 32 ? evict_select_kernel<32>
+                                     : evict_select_kernel<0>,
+                        p, cluster, s);
     if (err != cudaSuccess) return err;
-    const uint32_t blocks = (p.max_moves + 31) / 32;
+    const uint32_t blocks = (p.max_moves + 8 * kTogether - 1) / (8 * kTogether);
+    const uint32_t most = lists >= 64 ? 16 : 64;
     return launch_dependent(p.pool.dim == 64 ? evict_move_kernel<64> : evict_move_kernel<128>,
-                            dim3(blocks < 64 ? blocks : 64, p.pool.heads, p.batch), dim3(256), 0, s, p);
+                            dim3(blocks < most ? blocks : most, p.pool.heads, p.batch), dim3(256), 0, s, p);
 }
 
 }  // namespace sz
