@@ -87,9 +87,8 @@ struct Slots {
 template <int KEYS>
 __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictParams p) {
     __shared__ uint32_t s_bins[kCopies * kBins];
-    __shared__ uint32_t s_total[kBins];
-    __shared__ uint32_t s_count[kWarps];
-    __shared__ uint32_t s_sum[4];  // of the block: protected, ties, holes, movers
+    __shared__ uint32_t s_count[2][kWarps];
+    __shared__ uint32_t s_sum[3][2];  // of the block: protected; ties; holes and movers
     __shared__ uint32_t s_pick[2];
     wait_for_previous();
     const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31u;
@@ -139,38 +138,36 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictPa
             }
         }
     };
-    // Sum over the block's warps of x (one value per warp), in s_sum[k], and
-    // what the warps and blocks before this warp have.
-    auto place = [&](uint32_t x, int k, uint32_t& all) {
-        if (lane == 0) s_count[warp] = x;
+    // Turns two counts per warp into what the warps and blocks before this one
+    // have; returns the first's sum over the cluster.  k: a place of s_sum of
+    // its own.
+    auto place = [&](uint32_t& x, uint32_t& y, int k) {
+        if (lane == 0) s_count[0][warp] = x, s_count[1][warp] = y;
         __syncthreads();
-        if (warp == 0) {
-            uint32_t upto = s_count[lane];
-#pragma unroll
-            for (int d = 1; d < 32; d *= 2) {
-                const uint32_t o = __shfl_up_sync(0xFFFFFFFFu, upto, d);
-                if (lane >= (uint32_t)d) upto += o;
-            }
-            s_count[lane] = upto;
-            if (lane == 31) s_sum[k] = upto;
+        const uint32_t cx = s_count[0][lane], cy = s_count[1][lane];
+        x = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? cx : 0u);
+        y = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? cy : 0u);
+        uint32_t all_x = __reduce_add_sync(0xFFFFFFFFu, cx), all_y = __reduce_add_sync(0xFFFFFFFFu, cy);
+        if (blocks == 1) {
+            __syncthreads();  // s_count is written again by the next call
+            return all_x;
         }
+        if (tid == 0) s_sum[k][0] = all_x, s_sum[k][1] = all_y;
         cluster_sync();
-        uint32_t before = warp ? s_count[warp - 1] : 0u;
-        all = 0;
+        all_x = 0;
         for (uint32_t r = 0; r < blocks; r++) {
-            const uint32_t v = peer_word(&s_sum[k], r);
-            all += v;
-            if (r < rank) before += v;
+            const uint32_t vx = peer_word(&s_sum[k][0], r), vy = peer_word(&s_sum[k][1], r);
+            all_x += vx;
+            if (r < rank) x += vx, y += vy;
         }
-        __syncthreads();  // s_count is written again by the next call
-        return before;
+        return all_x;
     };
 
     // ---- keys, and the protected ones' number ----
     load_keys();
-    uint32_t mine = 0, safe = 0;
+    uint32_t mine = 0, none = 0;
     each([&](uint32_t, uint32_t k, bool in) { mine += __popc(__ballot_sync(0xFFFFFFFFu, in && k == kProtected)); });
-    place(mine, 0, safe);
+    const uint32_t safe = place(mine, none, 0);
     if (safe >= p.keep) {
         only_safe = true;
         load_keys();
@@ -208,34 +205,43 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictPa
                 s_bins[i] = sum;
             }
         }
-        cluster_sync();
-        for (uint32_t i = tid; i < width; i += kThreads) {
-            uint32_t sum = 0;
-            for (uint32_t r = 0; r < blocks; r++) sum += peer_word(&s_bins[i], r);
-            s_total[i] = sum;
+        if (blocks > 1)
+            cluster_sync();
+        else
+            __syncthreads();
+        // The bin that holds the need-th largest.  Thread t has bins 2 t and
+        // 2 t + 1 from the top, of all blocks.
+        uint32_t two[2] = {0, 0};
+        if (2 * tid < width) {
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+                const uint32_t* bin = &s_bins[width - 1 - 2 * tid - e];
+                if (blocks == 1) {
+                    two[e] = *bin;
+                } else {
+                    for (uint32_t r = 0; r < blocks; r++) two[e] += peer_word(bin, r);
+                }
+            }
+        }
+        uint32_t upto = two[0] + two[1];
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const uint32_t o = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+            if (lane >= (uint32_t)d) upto += o;
+        }
+        if (lane == 31) s_count[0][warp] = upto;
+        __syncthreads();
+        const uint32_t others = s_count[0][lane];
+        upto += __reduce_add_sync(0xFFFFFFFFu, lane < warp ? others : 0u);
+        const uint32_t past = upto - two[0] - two[1];  // in higher bins
+        if (past < need && need <= upto) {
+            const bool second = need > past + two[0];
+            s_pick[0] = width - 1 - 2 * tid - (second ? 1u : 0u);
+            s_pick[1] = need - past - (second ? two[0] : 0u);
         }
         // No block clears its bins while another reads them.
-        cluster_sync();
-        // Warp 0 finds the bin that holds the need-th largest: each lane sums
-        // a run of bins, top lane first.
-        if (warp == 0) {
-            const uint32_t per = width / 32, hi = width - lane * per;
-            uint32_t sum = 0;
-            for (uint32_t j = 1; j <= per; j++) sum += s_total[hi - j];
-            uint32_t upto = sum;
-#pragma unroll
-            for (int d = 1; d < 32; d *= 2) {
-                const uint32_t o = __shfl_up_sync(0xFFFFFFFFu, upto, d);
-                if (lane >= (uint32_t)d) upto += o;
-            }
-            const uint32_t past = __ballot_sync(0xFFFFFFFFu, upto >= need);
-            if (past && lane == (uint32_t)(__ffs(past) - 1)) {
-                uint32_t left = need - (upto - sum), j = 1;
-                while (j < per && s_total[hi - j] < left) left -= s_total[hi - j], j++;
-                s_pick[0] = hi - j;
-                s_pick[1] = left;
-            }
-        }
+        if (blocks > 1)
+            cluster_sync();
         __syncthreads();
         threshold |= s_pick[0] << shift;
         fixed |= (width - 1) << shift;
@@ -244,9 +250,9 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictPa
 
     // ---- survivors, holes and movers, in slot order ----
     const uint32_t below = (1u << lane) - 1u;
-    uint32_t ties = 0, all = 0;
-    each([&](uint32_t, uint32_t k, bool in) { ties += __popc(__ballot_sync(0xFFFFFFFFu, in && k == threshold)); });
-    const uint32_t ties_before = place(ties, 1, all);
+    uint32_t ties_before = 0;
+    each([&](uint32_t, uint32_t k, bool in) { ties_before += __popc(__ballot_sync(0xFFFFFFFFu, in && k == threshold)); });
+    place(ties_before, none, 1);
     // Calls f(slot, holes, movers) for the warp's slots, with the ballots.
     auto sort_out = [&](auto f) {
         uint32_t tie = ties_before;
@@ -257,11 +263,10 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictPa
             f(i, __ballot_sync(0xFFFFFFFFu, in && i < p.keep && !stays), __ballot_sync(0xFFFFFFFFu, i >= p.keep && stays));
         });
     };
-    uint32_t holes = 0, movers = 0;
-    sort_out([&](uint32_t, uint32_t hb, uint32_t mb) { holes += __popc(hb), movers += __popc(mb); });
-    uint32_t hole = place(holes, 2, all);
-    if (tid == 0 && rank == 0) p.moves[list] = min(all, p.max_moves);
-    uint32_t mover = place(movers, 3, all);
+    uint32_t hole = 0, mover = 0;
+    sort_out([&](uint32_t, uint32_t hb, uint32_t mb) { hole += __popc(hb), mover += __popc(mb); });
+    const uint32_t holes = place(hole, mover, 2);
+    if (tid == 0 && rank == 0) p.moves[list] = min(holes, p.max_moves);
     uint32_t* to_list = p.pairs + 2ull * list * p.max_moves;
     uint32_t* from_list = to_list + p.max_moves;
     sort_out([&](uint32_t i, uint32_t hb, uint32_t mb) {
@@ -271,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictPa
         hole += __popc(hb);
         mover += __popc(mb);
     });
-    cluster_sync();  // no block leaves while another reads its counts
+    if (blocks > 1) cluster_sync();  // no block leaves while another reads its counts
 }
 
 constexpr uint32_t kTogether = 4;  // moves of a warp at a time
@@ -370,7 +375,7 @@ cudaError_t launch_evict(const EvictParams& p, cudaStream_t s) {
                         p, cluster, s);
     if (err != cudaSuccess) return err;
     const uint32_t blocks = (p.max_moves + 8 * kTogether - 1) / (8 * kTogether);
-    const uint32_t most = lists >= 64 ? 16 : 64;
+    const uint32_t most = lists >= 64 ? 48 : 64;
     return launch_dependent(p.pool.dim == 64 ? evict_move_kernel<64> : evict_move_kernel<128>,
                             dim3(blocks < most ? blocks : most, p.pool.heads, p.batch), dim3(256), 0, s, p);
 }
