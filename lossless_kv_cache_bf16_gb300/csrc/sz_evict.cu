@@ -88,7 +88,8 @@ template <int KEYS>
 __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictParams p) {
     __shared__ uint32_t s_bins[kCopies * kBins];
     __shared__ uint32_t s_count[2][kWarps];
-    __shared__ uint32_t s_sum[3][2];  // of the block: protected; ties; holes and movers
+    __shared__ uint32_t s_sum[2][2];  // of the block: ties; holes and movers
+    __shared__ uint32_t s_safe;       // the block's protected tokens
     __shared__ uint32_t s_pick[2];
     wait_for_previous();
     const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31u;
@@ -163,27 +164,24 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictPa
         return all_x;
     };
 
-    // ---- keys, and the protected ones' number ----
-    load_keys();
-    uint32_t mine = 0, none = 0;
-    each([&](uint32_t, uint32_t k, bool in) { mine += __popc(__ballot_sync(0xFFFFFFFFu, in && k == kProtected)); });
-    const uint32_t safe = place(mine, none, 0);
-    if (safe >= p.keep) {
-        only_safe = true;
-        load_keys();
-    }
-
     // ---- the threshold: `need` of the tokens whose key equals it survive ----
-    const uint32_t apart = only_safe ? 0u : kProtected;  // keys that do not compete
-    uint32_t threshold = 0, need = only_safe ? p.keep : p.keep - safe;
+    // Each level has bins of its own, so that none are cleared while another
+    // block reads them: levels 1 and 2 take the first one's spare copies.
+    load_keys();
+    uint32_t apart = kProtected;  // keys that do not compete
+    uint32_t threshold = 0, need = 0;
     uint32_t fixed = 0;  // mask of the bits chosen so far
     for (int level = 0; level < 3; level++) {
         const int shift = level == 0 ? 21 : level == 1 ? 10 : 0;
-        const uint32_t width = level == 2 ? 1024 : 2048, copies = level == 0 ? kCopies : 1;
-        for (uint32_t i = tid; i < copies * kBins; i += kThreads) s_bins[i] = 0;
+        const uint32_t width = level == 2 ? 1024 : 2048;
+        uint32_t* own = s_bins + level * kBins;
+        for (uint32_t i = tid; i < (level == 0 ? kCopies : 1) * kBins; i += kThreads) own[i] = 0;
+        if (level == 0 && tid == 0) s_safe = 0;
         __syncthreads();
-        uint32_t* bins = s_bins + (level == 0 ? lane % kCopies * kBins : 0);
+        uint32_t* bins = own + (level == 0 ? lane % kCopies * kBins : 0);
+        uint32_t safe = 0;
         each([&](uint32_t, uint32_t k, bool in) {
+            safe += in && k == kProtected;
             in = in && k != apart && (k & fixed) == threshold;
             const uint32_t bin = (k >> shift) & (width - 1);
             const uint32_t who = __ballot_sync(0xFFFFFFFFu, in);
@@ -192,30 +190,53 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictPa
             const uint32_t lead = __ffs(who) - 1;
             const uint32_t bin0 = __shfl_sync(0xFFFFFFFFu, bin, lead);
             if (__all_sync(0xFFFFFFFFu, !in || bin == bin0)) {
-                if (lane == lead) atomicAdd(&s_bins[bin0], __popc(who));
+                if (lane == lead) atomicAdd(&own[bin0], __popc(who));
             } else if (in) {
                 atomicAdd(&bins[bin], 1u);
             }
         });
+        if (level == 0) {
+            safe = __reduce_add_sync(0xFFFFFFFFu, safe);
+            if (lane == 0 && safe) atomicAdd(&s_safe, safe);
+        }
         __syncthreads();
         if (level == 0) {
             for (uint32_t i = tid; i < kBins; i += kThreads) {
                 uint32_t sum = 0;
-                for (uint32_t c = 0; c < kCopies; c++) sum += s_bins[c * kBins + i];
-                s_bins[i] = sum;
+                for (uint32_t c = 0; c < kCopies; c++) sum += own[c * kBins + i];
+                own[i] = sum;
             }
         }
         if (blocks > 1)
             cluster_sync();
         else
             __syncthreads();
+        if (level == 0 && !only_safe) {
+            safe = 0;
+            for (uint32_t r = 0; r < blocks; r++) safe += peer_word(&s_safe, r);
+            need = p.keep - safe;
+            if (safe >= p.keep) {
+                // The protected tokens are enough: they compete, and no other
+                // stays.  Once more from the start.
+                only_safe = true;
+                apart = 0;
+                need = p.keep;
+                if (blocks > 1)
+                    cluster_sync();
+                else
+                    __syncthreads();
+                load_keys();
+                level = -1;
+                continue;
+            }
+        }
         // The bin that holds the need-th largest.  Thread t has bins 2 t and
         // 2 t + 1 from the top, of all blocks.
         uint32_t two[2] = {0, 0};
         if (2 * tid < width) {
 #pragma unroll
             for (int e = 0; e < 2; e++) {
-                const uint32_t* bin = &s_bins[width - 1 - 2 * tid - e];
+                const uint32_t* bin = &own[width - 1 - 2 * tid - e];
                 if (blocks == 1) {
                     two[e] = *bin;
                 } else {
@@ -239,9 +260,6 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictPa
             s_pick[0] = width - 1 - 2 * tid - (second ? 1u : 0u);
             s_pick[1] = need - past - (second ? two[0] : 0u);
         }
-        // No block clears its bins while another reads them.
-        if (blocks > 1)
-            cluster_sync();
         __syncthreads();
         threshold |= s_pick[0] << shift;
         fixed |= (width - 1) << shift;
@@ -250,9 +268,9 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictPa
 
     // ---- survivors, holes and movers, in slot order ----
     const uint32_t below = (1u << lane) - 1u;
-    uint32_t ties_before = 0;
+    uint32_t ties_before = 0, none = 0;
     each([&](uint32_t, uint32_t k, bool in) { ties_before += __popc(__ballot_sync(0xFFFFFFFFu, in && k == threshold)); });
-    place(ties_before, none, 1);
+    place(ties_before, none, 0);
     // Calls f(slot, holes, movers) for the warp's slots, with the ballots.
     auto sort_out = [&](auto f) {
         uint32_t tie = ties_before;
@@ -265,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictPa
     };
     uint32_t hole = 0, mover = 0;
     sort_out([&](uint32_t, uint32_t hb, uint32_t mb) { hole += __popc(hb), mover += __popc(mb); });
-    const uint32_t holes = place(hole, mover, 2);
+    const uint32_t holes = place(hole, mover, 1);
     if (tid == 0 && rank == 0) p.moves[list] = min(holes, p.max_moves);
     uint32_t* to_list = p.pairs + 2ull * list * p.max_moves;
     uint32_t* from_list = to_list + p.max_moves;
