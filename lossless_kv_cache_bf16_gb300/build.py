@@ -1,7 +1,8 @@
 """In-tree build of ``libsplitzip.so`` (CUDA kernels + C ABI) for sm_103a.
 
 Each ``.cu`` file under ``csrc/`` is compiled in parallel with nvcc, then the
-objects are linked into a shared library next to this file.  A stamp file with
+objects are linked into a shared library next to this file.  ``sz_bind.cpp``,
+the C++ part of the Python binding, becomes the module ``_sz_bind`` beside it.  A stamp file with
 a hash of the sources and flags makes the build a no-op when nothing changed.
 ptxas resource usage (registers, spills, shared memory) is kept in
 ``_build/ptxas.log``.
@@ -14,6 +15,8 @@ import hashlib
 import os
 import shutil
 import subprocess
+import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -21,6 +24,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIBRARY = os.path.join(PKG, "libsplitzip.so")
+BINDING = os.path.join(PKG, "_sz_bind.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + [
@@ -43,11 +47,12 @@ def _sources():
 def _digest() -> str:
     h = hashlib.sha256()
     for path in sorted(_sources() + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh"))
-                       + glob.glob(os.path.join(INCLUDE, "*.h"))):
+                       + glob.glob(os.path.join(CSRC, "*.cpp")) + glob.glob(os.path.join(INCLUDE, "*.h"))):
         h.update(os.path.basename(path).encode())
         with open(path, "rb") as f:
             h.update(f.read())
     h.update(" ".join(NVCC_FLAGS).encode())
+    h.update(sys.version.encode())  # the binding is built for this interpreter
     return h.hexdigest()
 
 
@@ -55,7 +60,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     """Compile and link the library if the sources changed; return its path."""
     stamp = LIBRARY + ".stamp"
     want = _digest()
-    if not force and os.path.exists(LIBRARY) and os.path.exists(stamp):
+    if not force and os.path.exists(LIBRARY) and os.path.exists(BINDING) and os.path.exists(stamp):
         with open(stamp) as f:
             if f.read().strip() == want:
                 return LIBRARY
@@ -69,8 +74,21 @@ def build(force: bool = False, verbose: bool = False) -> str:
             raise RuntimeError(f"nvcc failed on {os.path.basename(src)}:\n{res.stdout}\n{res.stderr}")
         return obj, res.stderr
 
+    def compile_binding():
+        part = BINDING + f".{os.getpid()}.part"
+        cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-Wall", "-shared", "-fPIC", "-fvisibility=hidden",
+               f"-I{sysconfig.get_paths()['include']}", f"-I{INCLUDE}",
+               f"-I{os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(exe))), 'include')}",
+               os.path.join(CSRC, "sz_bind.cpp"), "-o", part]
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        if res.returncode != 0:
+            raise RuntimeError(f"g++ failed on sz_bind.cpp:\n{res.stdout}\n{res.stderr}")
+        os.replace(part, BINDING)
+
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as pool:
+        binding = pool.submit(compile_binding)
         results = list(pool.map(compile_one, _sources()))
+        binding.result()
     with open(os.path.join(BUILD_DIR, "ptxas.log"), "w") as f:
         for _, log in results:
             f.write(log)

@@ -1,0 +1,196 @@
+// sz_bind.cpp -- the part of the Python binding that every call of a serving
+// operator goes through, in C++: checks of tensor arguments, and the calls of
+// the C ABI.  Interpreted, they cost more time than a decode step's kernels.
+//
+// It sees tensors only through their Python attributes (dtype, shape,
+// stride(), is_cuda, is_contiguous(), data_ptr()), and the library only
+// through the addresses that splitzip.py passes, so that it depends on neither
+// PyTorch's headers nor the order in which libraries are loaded.
+#define PY_SSIZE_T_CLEAN
+#include <Python.h>
+
+#include <cstdint>
+#include <cstring>
+
+#include "splitzip.h"
+
+namespace {
+
+PyObject *s_dtype, *s_shape, *s_stride, *s_is_cuda, *s_is_contiguous, *s_data_ptr, *s_numel;
+
+// An owned reference.
+struct Ref {
+    PyObject* o;
+    explicit Ref(PyObject* p = nullptr) : o(p) {}
+    ~Ref() { Py_XDECREF(o); }
+    Ref(const Ref&) = delete;
+    Ref& operator=(const Ref&) = delete;
+    explicit operator bool() const { return o != nullptr; }
+};
+
+// 1 or 0 for a truth value (its reference is taken over), -1 with an error.
+int truth(PyObject* o) {
+    if (!o) return -1;
+    const int r = PyObject_IsTrue(o);
+    Py_DECREF(o);
+    return r;
+}
+
+PyObject* refuse(PyObject* what, const char* why) {
+    if (!PyErr_Occurred()) PyErr_Format(PyExc_ValueError, "%U %s", what, why);
+    return nullptr;
+}
+
+bool expect(Py_ssize_t got, Py_ssize_t want) {
+    if (got == want) return true;
+    PyErr_Format(PyExc_TypeError, "%zd arguments expected, not %zd", want, got);
+    return false;
+}
+
+// rows(t, bfloat16, what) -> (data_ptr, shape, stride) of a bf16 CUDA tensor
+// [rows, heads, channels] whose channels are contiguous.
+PyObject* rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    if (!expect(n, 3)) return nullptr;
+    PyObject *t = a[0], *what = a[2];
+    Ref dtype(PyObject_GetAttr(t, s_dtype)), shape(PyObject_GetAttr(t, s_shape)), stride(PyObject_CallMethodNoArgs(t, s_stride));
+    if (!dtype || !shape || !stride) return nullptr;
+    if (dtype.o != a[1] || !PyTuple_Check(shape.o) || !PyTuple_Check(stride.o) || PyTuple_GET_SIZE(shape.o) != 3 ||
+        PyTuple_GET_SIZE(stride.o) != 3)
+        return refuse(what, "must be a bfloat16 tensor of three dimensions");
+    const int cuda = truth(PyObject_GetAttr(t, s_is_cuda));
+    if (cuda < 0) return nullptr;
+    if (!cuda) return refuse(what, "must be a CUDA tensor");
+    const long long last = PyLong_AsLongLong(PyTuple_GET_ITEM(stride.o, 2));
+    if (last != 1) {
+        if (PyErr_Occurred()) return nullptr;
+        bool empty = false;
+        for (int k = 0; k < 3; k++) empty |= PyLong_AsLongLong(PyTuple_GET_ITEM(shape.o, k)) == 0;
+        if (PyErr_Occurred()) return nullptr;
+        if (!empty) return refuse(what, "must have contiguous channels");
+    }
+    Ref ptr(PyObject_CallMethodNoArgs(t, s_data_ptr));
+    if (!ptr) return nullptr;
+    return PyTuple_Pack(3, ptr.o, shape.o, stride.o);
+}
+
+// pointer(t, dtype or None, count or -1, what) -> data_ptr of a contiguous CUDA
+// tensor of that type with that many values; None for None.
+PyObject* pointer(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    if (!expect(n, 4)) return nullptr;
+    PyObject *t = a[0], *what = a[3];
+    if (t == Py_None) Py_RETURN_NONE;
+    if (a[1] != Py_None) {
+        Ref dtype(PyObject_GetAttr(t, s_dtype));
+        if (!dtype) return nullptr;
+        if (dtype.o != a[1]) {
+            PyErr_Format(PyExc_ValueError, "%U must be %S", what, a[1]);
+            return nullptr;
+        }
+    }
+    const long long want = PyLong_AsLongLong(a[2]);
+    if (want == -1 && PyErr_Occurred()) return nullptr;
+    if (want >= 0) {
+        Ref numel(PyObject_CallMethodNoArgs(t, s_numel));
+        if (!numel) return nullptr;
+        const long long got = PyLong_AsLongLong(numel.o);
+        if (got == -1 && PyErr_Occurred()) return nullptr;
+        if (got != want) {
+            PyErr_Format(PyExc_ValueError, "%U must hold %lld values, not %lld", what, want, got);
+            return nullptr;
+        }
+    }
+    const int cuda = truth(PyObject_GetAttr(t, s_is_cuda));
+    if (cuda < 0) return nullptr;
+    if (!cuda) return refuse(what, "must be a CUDA tensor");
+    const int dense = truth(PyObject_CallMethodNoArgs(t, s_is_contiguous));
+    if (dense < 0) return nullptr;
+    if (!dense) return refuse(what, "must be contiguous");
+    return PyObject_CallMethodNoArgs(t, s_data_ptr);
+}
+
+// ---- calls: the function's address, then its arguments ----------------------
+// Pointers are integers or None, the stream the last one.  Bad Python values
+// leave an error that is looked at once, before the call.
+void* as_ptr(PyObject* o) { return o == Py_None ? nullptr : PyLong_AsVoidPtr(o); }
+int64_t as_int(PyObject* o) { return PyLong_AsLongLong(o); }
+size_t as_size(PyObject* o) { return PyLong_AsSize_t(o); }
+float as_float(PyObject* o) { return (float)PyFloat_AsDouble(o); }
+
+template <typename F>
+F* address(PyObject* o) {
+    return reinterpret_cast<F*>(PyLong_AsVoidPtr(o));
+}
+
+#define P(k) as_ptr(a[k])
+#define I(k) as_int(a[k])
+#define Z(k) as_size(a[k])
+
+// Evaluates the arguments, then calls, unless one of them was bad.
+template <typename F, typename... Args>
+PyObject* invoke(F* f, Args... args) {
+    if (PyErr_Occurred()) return nullptr;
+    if (!f) {
+        PyErr_SetString(PyExc_ValueError, "no function");
+        return nullptr;
+    }
+    return PyLong_FromLong((long)f(args...));
+}
+
+template <typename T>
+T* to(void* p) {
+    return static_cast<T*>(p);
+}
+
+PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    if (!expect(n, 25)) return nullptr;
+    return invoke(address<decltype(sz_qk_norm_rope)>(a[0]), P(1), I(2), I(3), Z(4), P(5), I(6), I(7), Z(8), Z(9), Z(10), P(11),
+                  P(12), as_float(a[13]), to<const float>(P(14)), Z(15), (int)I(16), to<const int32_t>(P(17)), P(18), I(19),
+                  I(20), P(21), I(22), I(23), to<CUstream_st>(P(24)));
+}
+
+PyObject* cache_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    if (!expect(n, 19)) return nullptr;
+    return invoke(address<decltype(sz_cache_append)>(a[0]), P(1), I(2), I(3), P(4), I(5), I(6), Z(7), to<const int64_t>(P(8)),
+                  to<const int32_t>(P(9)), P(10), Z(11), Z(12), Z(13), Z(14), to<float>(P(15)), to<int32_t>(P(16)),
+                  to<int>(P(17)), to<CUstream_st>(P(18)));
+}
+
+PyObject* cache_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    if (!expect(n, 16)) return nullptr;
+    return invoke(address<decltype(sz_cache_read)>(a[0]), P(1), Z(2), Z(3), Z(4), Z(5), to<const int64_t>(P(6)), Z(7), P(8),
+                  I(9), I(10), P(11), I(12), I(13), to<int>(P(14)), to<CUstream_st>(P(15)));
+}
+
+PyObject* cache_attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    if (!expect(n, 24)) return nullptr;
+    return invoke(address<decltype(sz_cache_attend)>(a[0]), P(1), I(2), I(3), Z(4), Z(5), P(6), Z(7), Z(8), Z(9), Z(10),
+                  to<const int32_t>(P(11)), Z(12), to<const int32_t>(P(13)), as_float(a[14]), P(15), I(16), I(17),
+                  to<float>(P(18)), to<float>(P(19)), to<int>(P(20)), P(21), Z(22), to<CUstream_st>(P(23)));
+}
+
+PyObject* cache_evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    if (!expect(n, 20)) return nullptr;
+    return invoke(address<decltype(sz_cache_evict)>(a[0]), P(1), Z(2), Z(3), Z(4), Z(5), to<const int32_t>(P(6)), Z(7),
+                  to<const int32_t>(P(8)), to<const int32_t>(P(9)), Z(10), Z(11), Z(12), to<float>(P(13)), to<int32_t>(P(14)),
+                  to<int32_t>(P(15)), to<int>(P(16)), P(17), Z(18), to<CUstream_st>(P(19)));
+}
+
+#define FAST(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(name)), METH_FASTCALL, nullptr}
+PyMethodDef methods[] = {FAST(rows),        FAST(pointer),      FAST(qk_norm_rope), FAST(cache_append),
+                         FAST(cache_read),  FAST(cache_attend), FAST(cache_evict),  {nullptr, nullptr, 0, nullptr}};
+
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_sz_bind", "Checks and calls of splitzip.py's serving operators.", -1, methods,
+                      nullptr, nullptr, nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__sz_bind(void) {
+    struct {
+        PyObject** at;
+        const char* name;
+    } names[] = {{&s_dtype, "dtype"}, {&s_shape, "shape"}, {&s_stride, "stride"}, {&s_is_cuda, "is_cuda"},
+                 {&s_is_contiguous, "is_contiguous"}, {&s_data_ptr, "data_ptr"}, {&s_numel, "numel"}};
+    for (auto& x : names)
+        if (!(*x.at = PyUnicode_InternFromString(x.name))) return nullptr;
+    return PyModule_Create(&module);
+}

@@ -2,7 +2,8 @@
 
 Argument marshalling only: every function forwards to ``libsplitzip.so`` with
 the same name, passing device pointers of torch CUDA tensors and the current
-CUDA stream.  All work runs in the library's CUDA kernels; there is no CPU
+CUDA stream (through ctypes; the serving operators, which are called once a
+layer and token, through the C++ module ``_sz_bind``).  All work runs in the library's CUDA kernels; there is no CPU
 path, and importing this module fails loudly when the library is missing.
 """
 from __future__ import annotations
@@ -95,6 +96,11 @@ def _load() -> ctypes.CDLL:
 
 
 LIB = _load()
+
+from . import _sz_bind as _bind  # noqa: E402  (built with the library)
+
+_ADDRESS = {name: ctypes.cast(getattr(LIB, name), ctypes.c_void_p).value
+            for name in ("sz_qk_norm_rope", "sz_cache_append", "sz_cache_read", "sz_cache_attend", "sz_cache_evict")}
 
 
 # ---- marshalling helpers -----------------------------------------------------
@@ -414,43 +420,23 @@ def sz_debug_encode_stalled(dt: int, cb, x: torch.Tensor, out: torch.Tensor, out
 
 # ---- serving operators around the 4-bit paged KV cache -------------------------
 
-def _rows(t: torch.Tensor, what: str):
-    """Shape and strides of a bf16 CUDA tensor [rows, heads, head_dim] whose
-    channels are contiguous."""
-    if t.dtype is not torch.bfloat16 or t.dim() != 3:
-        raise ValueError(f"{what} must be a bfloat16 tensor of three dimensions")
-    if not t.is_cuda:
-        raise ValueError(f"{what} must be a CUDA tensor")
-    shape, stride = t.shape, t.stride()
-    if stride[2] != 1 and t.numel():
-        raise ValueError(f"{what} must have contiguous channels")
-    return shape, stride
+_BF16, _F32, _I32, _I64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
+_rows, _pointer = _bind.rows, _bind.pointer
 
 
-def _written_rows(t: torch.Tensor, shape, what: str):
-    """Strides of a tensor as _rows, of the given shape, that a kernel writes:
-    no two of its rows may share memory."""
-    got, stride = _rows(t, what)
-    if got != shape:
-        raise ValueError(f"{what} must have shape {tuple(shape)}, not {tuple(got)}")
+def _written_rows(t: torch.Tensor, want, what: str):
+    """_rows of a tensor of the given shape that a kernel writes: no two of its
+    rows may share memory."""
+    ptr, shape, stride = got = _rows(t, _BF16, what)
+    if shape != want:
+        raise ValueError(f"{what} must have shape {tuple(want)}, not {tuple(shape)}")
     if not t.is_contiguous():
         reach = 0
-        for s, n in sorted(x for x in zip(stride, got) if x[1] > 1):
+        for s, n in sorted(x for x in zip(stride, shape) if x[1] > 1):
             if s <= reach:
                 raise ValueError(f"{what} must not overlap itself")
             reach += s * (n - 1)
-    return stride
-
-
-def _typed(t: torch.Tensor | None, dtype: torch.dtype, numel: int, what: str):
-    """Pointer of a contiguous CUDA tensor of `dtype` with `numel` values (None stays None)."""
-    if t is None:
-        return None
-    if t.dtype is not dtype:
-        raise ValueError(f"{what} must be {str(dtype).removeprefix('torch.')}")
-    if t.numel() != numel:
-        raise ValueError(f"{what} must hold {numel} values, not {t.numel()}")
-    return _dev_ptr(t, what)
+    return got
 
 
 _PAGE_BYTES: dict = {}  # (head_dim, kv_heads, page_tokens) -> bytes of a page
@@ -472,7 +458,7 @@ def _table(table: torch.Tensor, batch: int):
     shape = table.shape
     if len(shape) != 2 or shape[0] != batch:
         raise ValueError("table must be [batch, pages of a sequence]")
-    return _typed(table, torch.int32, batch * shape[1], "table"), shape[1]
+    return _pointer(table, _I32, -1, "table"), shape[1]
 
 
 def sz_cache_page_bytes(head_dim: int, kv_heads: int, page_tokens: int) -> int:
@@ -485,22 +471,20 @@ def sz_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor | N
     """Per-head RMS norm (where a weight is given) and rotation of q [tokens,
     q heads, D] and k [tokens, kv heads, D] into q_out and k_out (which may be
     q and k).  inv_freq: fp32, one frequency per rotated pair."""
-    q_shape, qs = _rows(q, "q")
+    qp, q_shape, qs = _rows(q, _BF16, "q")
+    kp, k_shape, ks = _rows(k, _BF16, "k")
     tokens, q_heads, d = q_shape
-    k_shape, ks = _rows(k, "k")
     if k_shape[0] != tokens or k_shape[2] != d:
         raise ValueError("q and k must have the same tokens and head dimension")
-    qos, kos = _written_rows(q_out, q_shape, "q_out"), _written_rows(k_out, k_shape, "k_out")
-    qp, kp, qop, kop = q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr()
+    qop, _, qos = _written_rows(q_out, q_shape, "q_out")
+    kop, _, kos = _written_rows(k_out, k_shape, "k_out")
     if (qp == qop and qs != qos) or (kp == kop and ks != kos):
         raise ValueError("an output over its input must have the input's strides")
-    pairs = inv_freq.numel()
-    _check("sz_qk_norm_rope", LIB.sz_qk_norm_rope(
-        qp, qs[0], qs[1], q_heads, kp, ks[0], ks[1], k_shape[1], tokens, d,
-        _typed(q_weight, torch.bfloat16, d, "q_weight"), _typed(k_weight, torch.bfloat16, d, "k_weight"), eps,
-        _typed(inv_freq, torch.float32, pairs, "inv_freq"), 2 * pairs, int(interleaved),
-        _typed(positions, torch.int32, tokens, "positions"), qop, qos[0], qos[1], kop, kos[0], kos[1],
-        _stream(stream)))
+    _check("sz_qk_norm_rope", _bind.qk_norm_rope(
+        _ADDRESS["sz_qk_norm_rope"], qp, qs[0], qs[1], q_heads, kp, ks[0], ks[1], k_shape[1], tokens, d,
+        _pointer(q_weight, _BF16, d, "q_weight"), _pointer(k_weight, _BF16, d, "k_weight"), eps,
+        _pointer(inv_freq, _F32, -1, "inv_freq"), 2 * inv_freq.numel(), interleaved,
+        _pointer(positions, _I32, tokens, "positions"), qop, qos[0], qos[1], kop, kos[0], kos[1], _stream(stream)))
 
 
 def sz_cache_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, pool: torch.Tensor, page_tokens: int,
@@ -509,32 +493,32 @@ def sz_cache_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, pool:
     """Quantises k and v [tokens, kv heads, D] into the pool at `slots` (int64,
     page * page_tokens + offset; -1 leaves a token out).  weight (fp32) and pos
     (int32), one entry per page, kv head and offset, are set at those slots."""
-    shape, ks = _rows(k, "k")
-    tokens, heads, d = shape
-    v_shape, vs = _rows(v, "v")
+    kp, shape, ks = _rows(k, _BF16, "k")
+    vp, v_shape, vs = _rows(v, _BF16, "v")
     if v_shape != shape:
         raise ValueError("k and v must have the same shape")
     if pos is not None and positions is None:
         raise ValueError("pos needs positions")
+    tokens, heads, d = shape
     pages = _cache_pages(pool, heads, d, page_tokens)
     cells = pages * heads * page_tokens
-    _check("sz_cache_append", LIB.sz_cache_append(
-        k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], tokens, _typed(slots, torch.int64, tokens, "slots"),
-        _typed(positions, torch.int32, tokens, "positions"), _dev_ptr(pool, "pool"), pages, heads, d, page_tokens,
-        _typed(weight, torch.float32, cells, "weight"), _typed(pos, torch.int32, cells, "pos"),
-        _typed(status, torch.int32, 1, "status"), _stream(stream)))
+    _check("sz_cache_append", _bind.cache_append(
+        _ADDRESS["sz_cache_append"], kp, ks[0], ks[1], vp, vs[0], vs[1], tokens, _pointer(slots, _I64, tokens, "slots"),
+        _pointer(positions, _I32, tokens, "positions"), _pointer(pool, None, -1, "pool"), pages, heads, d, page_tokens,
+        _pointer(weight, _F32, cells, "weight"), _pointer(pos, _I32, cells, "pos"), _pointer(status, _I32, 1, "status"),
+        _stream(stream)))
 
 
 def sz_cache_read(pool: torch.Tensor, page_tokens: int, slots: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
                   status: torch.Tensor | None = None, stream=None) -> None:
     """Reads the values at `slots` into k and v [tokens, kv heads, D] as bf16."""
-    shape = k.shape
-    ks, vs = _written_rows(k, shape, "k"), _written_rows(v, shape, "v")
+    kp, shape, ks = _written_rows(k, k.shape, "k")
+    vp, _, vs = _written_rows(v, shape, "v")
     tokens, heads, d = shape
-    _check("sz_cache_read", LIB.sz_cache_read(
-        _dev_ptr(pool, "pool"), _cache_pages(pool, heads, d, page_tokens), heads, d, page_tokens,
-        _typed(slots, torch.int64, tokens, "slots"), tokens, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1],
-        _typed(status, torch.int32, 1, "status"), _stream(stream)))
+    _check("sz_cache_read", _bind.cache_read(
+        _ADDRESS["sz_cache_read"], _pointer(pool, None, -1, "pool"), _cache_pages(pool, heads, d, page_tokens), heads, d,
+        page_tokens, _pointer(slots, _I64, tokens, "slots"), tokens, kp, ks[0], ks[1], vp, vs[0], vs[1],
+        _pointer(status, _I32, 1, "status"), _stream(stream)))
 
 
 def sz_cache_attend_workspace_size(batch: int, q_heads: int, kv_heads: int, head_dim: int, max_tokens: int,
@@ -550,20 +534,18 @@ def sz_cache_attend(q: torch.Tensor, pool: torch.Tensor, kv_heads: int, page_tok
     cache: sequence b's lens[b] tokens lie in the pages table[b].  lse (fp32
     [batch, q heads]) gets the log-sums; weight (fp32, one entry per page, kv
     head and offset) grows by the attention weights."""
-    shape, qs = _rows(q, "q")
+    qp, shape, qs = _rows(q, _BF16, "q")
     batch, q_heads, d = shape
-    os = _written_rows(out, shape, "out")
-    qp, op = q.data_ptr(), out.data_ptr()
+    op, _, os = _written_rows(out, shape, "out")
     if qp == op and batch:
         raise ValueError("out must not be q")
     pages = _cache_pages(pool, kv_heads, d, page_tokens)
     table_ptr, width = _table(table, batch)
-    _check("sz_cache_attend", LIB.sz_cache_attend(
-        qp, qs[0], qs[1], batch, q_heads, _dev_ptr(pool, "pool"), pages, kv_heads, d, page_tokens, table_ptr, width,
-        _typed(lens, torch.int32, batch, "lens"), scale, op, os[0], os[1],
-        _typed(lse, torch.float32, batch * q_heads, "lse"),
-        _typed(weight, torch.float32, pages * kv_heads * page_tokens, "weight"),
-        _typed(status, torch.int32, 1, "status"), _dev_ptr(ws, "ws"), ws.numel() * ws.element_size(),
+    _check("sz_cache_attend", _bind.cache_attend(
+        _ADDRESS["sz_cache_attend"], qp, qs[0], qs[1], batch, q_heads, _pointer(pool, None, -1, "pool"), pages, kv_heads,
+        d, page_tokens, table_ptr, width, _pointer(lens, _I32, batch, "lens"), scale, op, os[0], os[1],
+        _pointer(lse, _F32, batch * q_heads, "lse"), _pointer(weight, _F32, pages * kv_heads * page_tokens, "weight"),
+        _pointer(status, _I32, 1, "status"), _pointer(ws, None, -1, "ws"), ws.numel() * ws.element_size(),
         _stream(stream)))
 
 
@@ -583,9 +565,9 @@ def sz_cache_evict(pool: torch.Tensor, kv_heads: int, head_dim: int, page_tokens
     table_ptr, width = _table(table, batch)
     if keep < 0 or recent < 0:
         raise ValueError("keep and recent must not be negative")
-    _check("sz_cache_evict", LIB.sz_cache_evict(
-        _dev_ptr(pool, "pool"), pages, kv_heads, head_dim, page_tokens, table_ptr, width,
-        _typed(lens, torch.int32, batch, "lens"), _typed(next_pos, torch.int32, batch, "next_pos"), batch, keep,
-        recent, _typed(weight, torch.float32, cells, "weight"), _typed(pos, torch.int32, cells, "pos"),
-        _typed(new_lens, torch.int32, batch, "new_lens"), _typed(status, torch.int32, 1, "status"),
-        _dev_ptr(ws, "ws"), ws.numel() * ws.element_size(), _stream(stream)))
+    _check("sz_cache_evict", _bind.cache_evict(
+        _ADDRESS["sz_cache_evict"], _pointer(pool, None, -1, "pool"), pages, kv_heads, head_dim, page_tokens, table_ptr,
+        width, _pointer(lens, _I32, batch, "lens"), _pointer(next_pos, _I32, batch, "next_pos"), batch, keep, recent,
+        _pointer(weight, _F32, cells, "weight"), _pointer(pos, _I32, cells, "pos"),
+        _pointer(new_lens, _I32, batch, "new_lens"), _pointer(status, _I32, 1, "status"), _pointer(ws, None, -1, "ws"),
+        ws.numel() * ws.element_size(), _stream(stream)))

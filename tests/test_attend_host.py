@@ -41,8 +41,8 @@ def test_nothing_to_do_launches_nothing(S):
 
 
 def test_binding_refuses_mismatched_tensors(S, monkeypatch):
-    rec = Recorder(S.LIB)
-    monkeypatch.setattr(S, "LIB", rec)
+    rec = Recorder(S._bind)
+    monkeypatch.setattr(S, "_bind", rec)
     i32, f32, u8 = torch.int32, torch.float32, torch.uint8
     t = fake
     pool = t(9, S.sz_cache_page_bytes(128, 2, 16), dtype=u8)
@@ -54,7 +54,7 @@ def test_binding_refuses_mismatched_tensors(S, monkeypatch):
                                                      table=t(4, 3, dtype=i32), lens=t(4, dtype=i32), scale=0.1, out=out,
                                                      ws=t(8, dtype=u8), stream=STREAM), **c})
     attend()
-    assert rec.calls == ["sz_cache_attend"]
+    assert rec.calls == ["cache_attend"]
     del rec.calls[:]
     for c in (dict(out=t(4, 8, 64)), dict(out=q), dict(table=t(3, 3, dtype=i32)), dict(table=t(4, 3, dtype=torch.int64)),
               dict(table=t(12, dtype=i32)), dict(table=t(4, 6, dtype=i32)[:, ::2]), dict(lens=t(3, dtype=i32)),

@@ -124,14 +124,13 @@ def fake(*shape, dtype=torch.bfloat16):
 
 
 class Recorder:
-    """Stands for the library: records the calls that would launch."""
+    """Stands for the binding's C++ part: checks tensors as it does and records
+    the calls that would launch."""
 
-    def __init__(self, lib):
-        self.lib, self.calls = lib, []
+    def __init__(self, bind):
+        self.rows, self.pointer, self.calls = bind.rows, bind.pointer, []
 
     def __getattr__(self, name):
-        if name in ("sz_cache_page_bytes", "sz_status_string"):
-            return getattr(self.lib, name)
         return lambda *a: self.calls.append(name) or 0
 
 
@@ -141,8 +140,8 @@ STREAM = type("Stream", (), {"cuda_stream": 0})()
 def test_binding_refuses_mismatched_tensors(S, monkeypatch):
     """Shapes, types and sizes that would let a kernel leave a buffer are
     refused by the binding; the library is not called."""
-    rec = Recorder(S.LIB)
-    monkeypatch.setattr(S, "LIB", rec)
+    rec = Recorder(S._bind)
+    monkeypatch.setattr(S, "_bind", rec)
     i32, i64, f32, u8 = torch.int32, torch.int64, torch.float32, torch.uint8
     t, s = fake, STREAM
     q, k = t(4, 8, 128), t(4, 2, 128)
@@ -185,6 +184,35 @@ def test_binding_refuses_mismatched_tensors(S, monkeypatch):
         with pytest.raises(ValueError):
             f(**c)
     assert rec.calls == []
+
+
+def test_bad_values_do_not_reach_the_library(S):
+    """Python values that are no numbers of the right kind raise; the call is
+    not made (address 0 would end the process if it were)."""
+    ok = [0, *APPEND.values()]
+    for at, bad in ((1, "x"), (2, 1.5), (7, -1), (7, None), (15, object()), (18, "stream")):
+        args = list(ok)
+        args[at] = bad
+        with pytest.raises((TypeError, OverflowError, ValueError)):
+            S._bind.cache_append(*args)
+    with pytest.raises(TypeError):
+        S._bind.cache_append(*ok[:-1])
+    with pytest.raises(ValueError):
+        S._bind.cache_append(*ok)
+    good = [S._ADDRESS["sz_cache_append"], *APPEND.values()]
+    good[7] = 0                                              # no tokens: nothing is launched
+    assert S._bind.cache_append(*good) == S.SZ_OK
+    good[10] = None
+    assert S._bind.cache_append(*good) == S.SZ_ERR_INVALID_ARG
+    for name, defaults in (("qk_norm_rope", NORM), ("cache_read", READ), ("cache_evict", EVICT)):
+        args = [S._ADDRESS["sz_" + name], *defaults.values()]
+        args[1 + list(defaults).index("dim")] = 96
+        assert getattr(S._bind, name)(*args) == S.SZ_ERR_INVALID_ARG
+    # A float argument arrives: a negative eps is refused, a good one passes.
+    args = [S._ADDRESS["sz_qk_norm_rope"], *{**NORM, "tokens": 0}.values()]
+    assert S._bind.qk_norm_rope(*args) == S.SZ_OK
+    args[1 + list(NORM).index("eps")] = -1.0
+    assert S._bind.qk_norm_rope(*args) == S.SZ_ERR_INVALID_ARG
 
 
 def test_signatures_cover_the_declared_arguments(S):
