@@ -52,6 +52,16 @@ __device__ __forceinline__ uint32_t peer_word(const uint32_t* p, uint32_t rank) 
     return v;
 }
 
+// Its sum over the first n blocks, with the loads under way together.
+__device__ __forceinline__ uint32_t peer_sum(const uint32_t* p, uint32_t n) {
+    uint32_t v[kMaxCluster], sum = 0;
+#pragma unroll
+    for (uint32_t r = 0; r < kMaxCluster; r++) v[r] = r < n ? peer_word(p, r) : 0u;
+#pragma unroll
+    for (uint32_t r = 0; r < kMaxCluster; r++) sum += v[r];
+    return sum;
+}
+
 // Unsigned order of the key = order of the weight; NaN counts as -infinity,
 // -0 as 0.  At most 0xFF800000 (+infinity), so protected tokens come first.
 __device__ __forceinline__ uint32_t key_of(float w) {
@@ -69,16 +79,36 @@ struct Slots {
         at = (((uint64_t)(uint32_t)page * p.pool.heads + h) << p.pool.lg_page) + (slot & ((1u << p.pool.lg_page) - 1u));
         return true;
     }
-    // only_safe: there are at least `keep` protected tokens, which compete by
-    // weight, and no other stays (key 0).
-    __device__ __forceinline__ uint32_t key(uint32_t slot, int64_t safe_from, bool only_safe) const {
-        uint64_t at;
-        if (!find(slot, at)) {
-            if (p.status) atomicMax(p.status, kStatusInvalid);
-            return 0;
+    // Keys of slots i0, i0 + 32, ... below `to`; 0 past it.  only_safe: there
+    // are at least `keep` protected tokens, which compete by weight, and no
+    // other stays (key 0).  All loads of a kind are under way together.
+    template <int N>
+    __device__ __forceinline__ void keys(uint32_t i0, uint32_t to, int64_t safe_from, bool only_safe, uint32_t* out) const {
+        uint64_t at[N];
+        int32_t page[N], pos[N];
+        float weight[N];
+        bool bad = false;
+        const int32_t* row = p.table + (uint64_t)b * p.table_width;
+#pragma unroll
+        for (int j = 0; j < N; j++) page[j] = i0 + 32 * j < to ? row[(i0 + 32 * j) >> p.pool.lg_page] : 0;
+#pragma unroll
+        for (int j = 0; j < N; j++) {
+            const bool ok = (uint32_t)page[j] < p.pool.pages;
+            bad |= !ok;
+            at[j] = (((uint64_t)(ok ? (uint32_t)page[j] : 0u) * p.pool.heads + h) << p.pool.lg_page) +
+                    ((i0 + 32 * j) & ((1u << p.pool.lg_page) - 1u));
         }
-        const bool safe = (int64_t)p.pos[at] >= safe_from;
-        return safe == only_safe ? key_of(p.weight[at]) : safe ? kProtected : 0u;
+#pragma unroll
+        for (int j = 0; j < N; j++) pos[j] = p.pos[at[j]];
+#pragma unroll
+        for (int j = 0; j < N; j++) weight[j] = p.weight[at[j]];
+#pragma unroll
+        for (int j = 0; j < N; j++) {
+            const bool safe = (int64_t)pos[j] >= safe_from;
+            const uint32_t k = safe == only_safe ? key_of(weight[j]) : safe ? kProtected : 0u;
+            out[j] = i0 + 32 * j < to && (uint32_t)page[j] < p.pool.pages ? k : 0u;
+        }
+        if (bad && p.status) atomicMax(p.status, kStatusInvalid);
     }
 };
 
@@ -116,11 +146,10 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictPa
     bool only_safe = false;
     auto load_keys = [&]() {
         if constexpr (KEYS > 0) {
+            constexpr int kBatch = KEYS < 8 ? KEYS : 8;
 #pragma unroll
-            for (int j = 0; j < KEYS; j++) {
-                const uint32_t i = from + 32 * j + lane;
-                keys[j] = i < to ? slots.key(i, safe_from, only_safe) : 0u;
-            }
+            for (int j = 0; j < KEYS; j += kBatch)
+                slots.keys<kBatch>(from + 32 * j + lane, to, safe_from, only_safe, keys + j);
         }
     };
     // Calls f(slot, key, whether there is such a slot) for the warp's slots in
@@ -134,8 +163,9 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictPa
             }
         } else {
             for (uint32_t i0 = from; i0 < to; i0 += 32) {
-                const bool in = i0 + lane < to;
-                f(i0 + lane, in ? slots.key(i0 + lane, safe_from, only_safe) : 0u, in);
+                uint32_t k;
+                slots.keys<1>(i0 + lane, to, safe_from, only_safe, &k);
+                f(i0 + lane, k, i0 + lane < to);
             }
         }
     };
@@ -155,12 +185,9 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictPa
         }
         if (tid == 0) s_sum[k][0] = all_x, s_sum[k][1] = all_y;
         cluster_sync();
-        all_x = 0;
-        for (uint32_t r = 0; r < blocks; r++) {
-            const uint32_t vx = peer_word(&s_sum[k][0], r), vy = peer_word(&s_sum[k][1], r);
-            all_x += vx;
-            if (r < rank) x += vx, y += vy;
-        }
+        x += peer_sum(&s_sum[k][0], rank);
+        y += peer_sum(&s_sum[k][1], rank);
+        all_x = peer_sum(&s_sum[k][0], blocks);
         return all_x;
     };
 
@@ -180,13 +207,13 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictPa
         __syncthreads();
         uint32_t* bins = own + (level == 0 ? lane % kCopies * kBins : 0);
         uint32_t safe = 0;
+        if (level == 0) each([&](uint32_t, uint32_t k, bool in) { safe += in && k == kProtected; });
         each([&](uint32_t, uint32_t k, bool in) {
-            safe += in && k == kProtected;
             in = in && k != apart && (k & fixed) == threshold;
+            if (!__any_sync(0xFFFFFFFFu, in)) return;
             const uint32_t bin = (k >> shift) & (width - 1);
-            const uint32_t who = __ballot_sync(0xFFFFFFFFu, in);
-            if (!who) return;
             // A warp whose keys share a bin (equal weights) adds once.
+            const uint32_t who = __ballot_sync(0xFFFFFFFFu, in);
             const uint32_t lead = __ffs(who) - 1;
             const uint32_t bin0 = __shfl_sync(0xFFFFFFFFu, bin, lead);
             if (__all_sync(0xFFFFFFFFu, !in || bin == bin0)) {
@@ -212,8 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictPa
         else
             __syncthreads();
         if (level == 0 && !only_safe) {
-            safe = 0;
-            for (uint32_t r = 0; r < blocks; r++) safe += peer_word(&s_safe, r);
+            safe = peer_sum(&s_safe, blocks);
             need = p.keep - safe;
             if (safe >= p.keep) {
                 // The protected tokens are enough: they compete, and no other
@@ -237,11 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictPa
 #pragma unroll
             for (int e = 0; e < 2; e++) {
                 const uint32_t* bin = &own[width - 1 - 2 * tid - e];
-                if (blocks == 1) {
-                    two[e] = *bin;
-                } else {
-                    for (uint32_t r = 0; r < blocks; r++) two[e] += peer_word(bin, r);
-                }
+                two[e] = blocks == 1 ? *bin : peer_sum(bin, blocks);
             }
         }
         uint32_t upto = two[0] + two[1];
