@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictPa
     __shared__ uint32_t s_count[2][kWarps];
     __shared__ uint32_t s_sum[2][2];  // of the block: ties; holes and movers
     __shared__ uint32_t s_safe;       // the block's protected tokens
-    __shared__ uint32_t s_pick[2];
+    __shared__ uint32_t s_pick[3];  // a bin, how many of its keys survive, how many it has
     wait_for_previous();
     const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31u;
     const uint32_t rank = cluster_rank(), blocks = cluster_size();
@@ -198,7 +198,8 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictPa
     uint32_t apart = kProtected;  // keys that do not compete
     uint32_t threshold = 0, need = 0;
     uint32_t fixed = 0;  // mask of the bits chosen so far
-    for (int level = 0; level < 3; level++) {
+    bool all_pass = false;
+    for (int level = 0; level < 3 && !all_pass; level++) {
         const int shift = level == 0 ? 21 : level == 1 ? 10 : 0;
         const uint32_t width = level == 2 ? 1024 : 2048;
         uint32_t* own = s_bins + level * kBins;
@@ -281,35 +282,61 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictPa
             const bool second = need > past + two[0];
             s_pick[0] = width - 1 - 2 * tid - (second ? 1u : 0u);
             s_pick[1] = need - past - (second ? two[0] : 0u);
+            s_pick[2] = second ? two[1] : two[0];
         }
         __syncthreads();
         threshold |= s_pick[0] << shift;
         fixed |= (width - 1) << shift;
         need = s_pick[1];
+        // All keys of the bin survive: with the lower bits at 0 the threshold
+        // lets them pass, and none has to be told from another.
+        all_pass = need == s_pick[2];
     }
 
     // ---- survivors, holes and movers, in slot order ----
     const uint32_t below = (1u << lane) - 1u;
     uint32_t ties_before = 0, none = 0;
-    each([&](uint32_t, uint32_t k, bool in) { ties_before += __popc(__ballot_sync(0xFFFFFFFFu, in && k == threshold)); });
-    place(ties_before, none, 0);
-    // Calls f(slot, holes, movers) for the warp's slots, with the ballots.
-    auto sort_out = [&](auto f) {
-        uint32_t tie = ties_before;
-        each([&](uint32_t i, uint32_t k, bool in) {
+    if (all_pass) {
+        need = 0xFFFFFFFFu;
+    } else {
+        each([&](uint32_t, uint32_t k, bool in) { ties_before += __popc(__ballot_sync(0xFFFFFFFFu, in && k == threshold)); });
+        place(ties_before, none, 0);
+    }
+    // What becomes of this lane's slots, a bit each (KEYS of them), or found
+    // again for the second pass.
+    uint32_t hole_bits = 0, mover_bits = 0, hole = 0, mover = 0, tie = ties_before;
+    auto sort_out = [&](uint32_t i, uint32_t k, bool in, uint32_t& hb, uint32_t& mb) {
+        bool stays = in && k >= threshold;
+        if (!all_pass) {
             const uint32_t eq = __ballot_sync(0xFFFFFFFFu, in && k == threshold);
-            const bool stays = in && (k > threshold || (k == threshold && tie + __popc(eq & below) < need));
+            stays = stays && (k != threshold || tie + __popc(eq & below) < need);
             tie += __popc(eq);
-            f(i, __ballot_sync(0xFFFFFFFFu, in && i < p.keep && !stays), __ballot_sync(0xFFFFFFFFu, i >= p.keep && stays));
-        });
+        }
+        hb = __ballot_sync(0xFFFFFFFFu, in && i < p.keep && !stays);
+        mb = __ballot_sync(0xFFFFFFFFu, i >= p.keep && stays);
     };
-    uint32_t hole = 0, mover = 0;
-    sort_out([&](uint32_t, uint32_t hb, uint32_t mb) { hole += __popc(hb), mover += __popc(mb); });
+    uint32_t bit = 0;
+    each([&](uint32_t i, uint32_t k, bool in) {
+        uint32_t hb, mb;
+        sort_out(i, k, in, hb, mb);
+        hole += __popc(hb), mover += __popc(mb);
+        if constexpr (KEYS > 0) hole_bits |= (hb >> lane & 1u) << bit, mover_bits |= (mb >> lane & 1u) << bit, bit++;
+    });
     const uint32_t holes = place(hole, mover, 1);
     if (tid == 0 && rank == 0) p.moves[list] = min(holes, p.max_moves);
     uint32_t* to_list = p.pairs + 2ull * list * p.max_moves;
     uint32_t* from_list = to_list + p.max_moves;
-    sort_out([&](uint32_t i, uint32_t hb, uint32_t mb) {
+    bit = 0;
+    tie = ties_before;
+    each([&](uint32_t i, uint32_t k, bool in) {
+        uint32_t hb, mb;
+        if constexpr (KEYS > 0) {
+            hb = __ballot_sync(0xFFFFFFFFu, hole_bits >> bit & 1u);
+            mb = __ballot_sync(0xFFFFFFFFu, mover_bits >> bit & 1u);
+            bit++;
+        } else {
+            sort_out(i, k, in, hb, mb);
+        }
         const uint32_t hi = hole + __popc(hb & below), mi = mover + __popc(mb & below);
         if (hb >> lane & 1u && hi < p.max_moves) to_list[hi] = i;
         if (mb >> lane & 1u && mi < p.max_moves) from_list[mi] = i;
