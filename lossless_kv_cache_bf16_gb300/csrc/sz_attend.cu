@@ -751,21 +751,35 @@ __global__ void __launch_bounds__(256) attend_weight_kernel(const AttendParams p
     if (len <= 0 || (uint64_t)len > max_tokens) return;
     const uint32_t q_heads = p.pool.heads * p.group;
     const uint64_t row0 = (uint64_t)b * q_heads + (uint64_t)kv_head * p.group;
-    for (uint32_t tok = (blockIdx.x * 256 + threadIdx.x) * 2; tok < (uint32_t)len; tok += gridDim.x * 512) {
+    const float* lse2 = p.lse2 + row0;
+    for (uint32_t tok = (blockIdx.x * 256 + threadIdx.x) * 4; tok < (uint32_t)len; tok += gridDim.x * 1024) {
         const int32_t page = p.table[(uint64_t)b * p.table_width + (tok >> p.pool.lg_page)];
         if ((uint32_t)page >= p.pool.pages) continue;
-        float w0 = 0.f, w1 = 0.f;
-#pragma unroll 4
-        for (uint32_t h = 0; h < p.group; h++) {
-            const float2 s = *reinterpret_cast<const float2*>(p.logits + (row0 + h) * max_tokens + tok);
-            const float lse2 = p.lse2[row0 + h];
-            w0 += exp2_fast(s.x - lse2);
-            w1 += exp2_fast(s.y - lse2);
+        const float* s = p.logits + row0 * max_tokens + tok;
+        float w[4] = {0.f, 0.f, 0.f, 0.f};
+        for (uint32_t h0 = 0; h0 < p.group; h0 += 8) {
+            float4 x[8];
+            float ref[8];
+#pragma unroll
+            for (uint32_t k = 0; k < 8; k++)
+                if (h0 + k < p.group) x[k] = *reinterpret_cast<const float4*>(s + (h0 + k) * max_tokens), ref[k] = lse2[h0 + k];
+#pragma unroll
+            for (uint32_t k = 0; k < 8; k++) {
+                if (h0 + k >= p.group) continue;
+                w[0] += exp2_fast(x[k].x - ref[k]), w[1] += exp2_fast(x[k].y - ref[k]);
+                w[2] += exp2_fast(x[k].z - ref[k]), w[3] += exp2_fast(x[k].w - ref[k]);
+            }
         }
         float* dst = p.weight + ((((uint64_t)(uint32_t)page * p.pool.heads + kv_head) << p.pool.lg_page) +
                                  (tok & ((1u << p.pool.lg_page) - 1u)));
-        atomicAdd(dst, w0);
-        if (tok + 1 < (uint32_t)len) atomicAdd(dst + 1, w1);
+        if (p.weight_vec && tok + 4 <= (uint32_t)len) {
+            asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(dst), "f"(w[0]), "f"(w[1]), "f"(w[2]), "f"(w[3])
+                         : "memory");
+        } else {
+#pragma unroll
+            for (uint32_t k = 0; k < 4; k++)
+                if (tok + k < (uint32_t)len) atomicAdd(dst + k, w[k]);
+        }
     }
 }
 
@@ -780,7 +794,7 @@ cudaError_t launch(const AttendParams& p, cudaStream_t s) {
     err = launch_dependent(attend_join_kernel<D>, dim3((uint32_t)sms), dim3(256), 0, s, p, (uint32_t)Sh::kHeads);
     if (err != cudaSuccess || !LOGITS) return err;
     const uint64_t tokens = (uint64_t)p.table_width << p.pool.lg_page;
-    const uint32_t blocks = (uint32_t)((tokens + 511) / 512);
+    const uint32_t blocks = (uint32_t)((tokens + 1023) / 1024);
     return launch_dependent(attend_weight_kernel, dim3(blocks < 1024 ? blocks : 1024, p.pool.heads, p.batch), dim3(256), 0, s, p);
 }
 

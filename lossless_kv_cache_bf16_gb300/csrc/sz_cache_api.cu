@@ -246,6 +246,7 @@ sz_status sz_cache_attend(const void* d_q, int64_t q_seq_stride, int64_t q_head_
     p.status = d_status;
     p.wait_limit_ns = kWaitLimitNs;
     p.q_vec = aligned(d_q, 16) && multiple(q_seq_stride, q_head_stride, 8);
+    p.weight_vec = aligned(d_weight, 16);
     p.out_vec = aligned(d_out, 8) && multiple(out_seq_stride, out_head_stride, 4);
     p.meta = reinterpret_cast<int32_t*>(ws);
     p.part_ml = reinterpret_cast<float*>(ws + w.ml);
