@@ -78,7 +78,7 @@ struct Left {
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -86,7 +86,7 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
 // The same into a fresh accumulator.
 __device__ __forceinline__ void mma_bf16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                                uint32_t b0, uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
@@ -108,7 +108,7 @@ __device__ __forceinline__ float scale_of(uint32_t w, uint32_t sel) { return __u
 // columns 2 c and 2 c + 1 of row r.
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     uint32_t y;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -301,6 +301,32 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attend_kernel(const
         in_flight++;
         batch_at++;
     };
+    // The query values of the item at `at`, this thread's share: the first
+    // item's are asked for before the ring's copies, behind which they would
+    // queue.
+    uint32_t q_raw[NT][kG][4];
+    auto fetch_q = [&](const Cursor& at) {
+        const uint32_t tile = at.item % p.tiles, first = at.item / p.tiles * p.group + tile * Sh::kHeads;
+#pragma unroll
+        for (int n = 0; n < NT; n++) {
+            const uint32_t h = g + 8 * n;
+            const uint16_t* q = p.q + (int64_t)at.b * p.q_seq + (int64_t)(first + h) * p.q_head + 8 * t;
+            const bool in = tile * Sh::kHeads + h < p.group;
+#pragma unroll
+            for (int i = 0; i < kG; i++) {
+#pragma unroll
+                for (int j = 0; j < 4; j++) q_raw[n][i][j] = 0;
+                if (in && p.q_vec) {
+                    const uint4 v = *reinterpret_cast<const uint4*>(q + 32 * i);
+                    q_raw[n][i][0] = v.x, q_raw[n][i][1] = v.y, q_raw[n][i][2] = v.z, q_raw[n][i][3] = v.w;
+                } else if (in) {
+#pragma unroll
+                    for (int j = 0; j < 4; j++) q_raw[n][i][j] = q[32 * i + 2 * j] | (uint32_t)q[32 * i + 2 * j + 1] << 16;
+                }
+            }
+        }
+    };
+    if (n_run) fetch_q(cur);
 #pragma unroll 1
     for (int k = 0; k < Sh::kStages; k++) issue(k);
     const uint32_t half_sel = g & 1u ? 0x3244u : 0x1044u;  // scales come in pairs of tokens
@@ -314,7 +340,10 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attend_kernel(const
         left -= take;
         cur.at += take;
         if (cur.at == cost) cur.next_item(items, s_len, p.batch);
-        if (r0 == r1) continue;
+        if (r0 == r1) {
+            if (left) fetch_q(cur);
+            continue;
+        }
         const bool starts = r0 == 0, ends = r1 == cost - kItemCost;
         const uint32_t kv_head = item / p.tiles, tile = item % p.tiles;
         const uint32_t head0 = kv_head * p.group + tile * Sh::kHeads;
@@ -325,26 +354,12 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attend_kernel(const
         float bias[kG][NT][2], mult[NT][2];  // of heads 2t and 2t + 1
 #pragma unroll
         for (int n = 0; n < NT; n++) {
-            const uint32_t h = g + 8 * n;
-            uint32_t x[kG][4];
+            uint32_t(&x)[kG][4] = q_raw[n];
             uint32_t top = 0;
 #pragma unroll
-            for (int i = 0; i < kG; i++) {
-                const uint16_t* src = p.q + (int64_t)seq * p.q_seq + (int64_t)(head0 + h) * p.q_head + 32 * i + 8 * t;
-#pragma unroll
-                for (int j = 0; j < 4; j++) x[i][j] = 0;
-                if (h < heads) {
-                    if (p.q_vec) {
-                        const uint4 v = *reinterpret_cast<const uint4*>(src);
-                        x[i][0] = v.x, x[i][1] = v.y, x[i][2] = v.z, x[i][3] = v.w;
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 4; j++) x[i][j] = src[2 * j] | (uint32_t)src[2 * j + 1] << 16;
-                    }
-                }
+            for (int i = 0; i < kG; i++)
 #pragma unroll
                 for (int j = 0; j < 4; j++) top = max(top, max(x[i][j] & 0x7FFFu, (x[i][j] >> 16) & 0x7FFFu));
-            }
             top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
             top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
             // Scaled by 2^(120 - up): the largest query value's exponent, or
@@ -638,6 +653,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attend_kernel(const
                 s_left[warp].rest = cost - kItemCost - r1;
             }
         }
+        if (left) fetch_q(cur);
     }
 
     // ---- join the pieces of items that several warps of this block hold ----
