@@ -16,8 +16,10 @@
 // once, in shared memory, for all heads.  D / 16 threads share a head's row,
 // each with two vectors of 8 channels: channels [8c, 8c + 8) and their
 // partners, so that a rotation never leaves a thread, and the sum of squares
-// is a shuffle over a few lanes.  A thread has the loads of two rows under
-// way.  Bound by memory.
+// is a shuffle over a few lanes.  Bound by memory: 48 warps per SM with one
+// row's loads each move more than 32 with two rows' (20,011 tokens of 28 and 4
+// heads of 128: 56 against 62 us, 86% of the measured copy rate; 8,192 of 32
+// and 8: 30 us, 81%).
 #include "sz_cache.cuh"
 #include "sz_params.h"
 
@@ -66,7 +68,7 @@ struct Item {
 };
 
 template <int D, bool VEC>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeParams p, const uint32_t tile) {
+__global__ void __launch_bounds__(kThreads, 6) norm_rope_kernel(const NormRopeParams p, const uint32_t tile) {
     constexpr uint32_t kPer = D / 16;              // threads of a row
     constexpr uint32_t kStep = kThreads / kPer;    // rows that the block takes at a time
     __shared__ float2 s_turn[kMaxTile * kMaxRot / 2];
@@ -174,12 +176,10 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeParam
                 store8<VEC>(it.dst + cb, b);
             }
         };
-        for (uint32_t done = 0; done < n * rows; done += 2 * kStep) {
-            Item x, y;
+        for (uint32_t done = 0; done < n * rows; done += kStep) {
+            Item x;
             next(x);
-            next(y);
             finish(x);
-            finish(y);
         }
         __syncthreads();
     }
