@@ -22,7 +22,7 @@
 namespace sz {
 namespace {
 
-constexpr uint32_t kThreads = 256;
+constexpr uint32_t kThreads = 128;
 constexpr uint32_t kTaskTokens = 8;
 
 // 2 N (4 or 8) bf16 values, two to a word.
@@ -362,7 +362,7 @@ cudaError_t launch(void (*kern)(AppendParams), const AppendParams& p, cudaStream
     const uint64_t tasks = ((uint64_t)p.tokens + kTaskTokens) / kTaskTokens * p.pool.heads;
     const uint64_t need = (tasks + kThreads / 32 - 1) / (kThreads / 32);
     const uint64_t fit = (uint64_t)sms * per_sm;
-    return launch_dependent(kern, dim3((uint32_t)(need < fit ? need : fit)), dim3(kThreads), 0, s, p);
+    return launch_dependent(kern, dim3((uint32_t)(need < 16 * fit ? need : 16 * fit)), dim3(kThreads), 0, s, p);
 }
 
 }  // namespace
