@@ -31,6 +31,13 @@
 // and writes the rows of an item that it holds whole.  Pieces of an item are
 // joined once per block in shared memory, pieces over several blocks by a
 // second kernel, both in list order: results do not depend on timing.
+//
+// Measured: each 8 sequences of 32,768 tokens more (4 kv heads of 128, 28
+// query heads, 151 MB) take 26 us, 5.7 TB/s or 85% of the copy rate, after
+// 8 to 9 us that any call takes (launch, lengths, first copies, joins).  About
+// 650 instructions per 32 tokens and warp; 12 warps per SM with 168 registers
+// are faster than 16 with 128 (62 against 64 us for 16 such sequences), and
+// the scales' and codes' unpacking keeps the integer pipe half busy.
 #include <type_traits>
 
 #include "sz_cache.cuh"

@@ -16,7 +16,9 @@
 // survive, holes and movers are counted, then numbered.  The blocks of a
 // cluster join their histograms and counts through each other's shared
 // memory.  Second kernel: the moves, four at a time to a warp.  Both are
-// bound by latency: 8 bytes a slot are read, and few tokens move.
+// bound by latency: 8 bytes a slot are read, and few tokens move (8 sequences
+// of 32,768 tokens, 4 heads, cut by a page: 18 us for the selection, 5 us for
+// the moves, against 1.3 us for their bytes).
 #include "sz_cache.cuh"
 #include "sz_params.h"
 
