@@ -133,7 +133,11 @@ PyObject* invoke(F* f, Args... args) {
         PyErr_SetString(PyExc_ValueError, "no function");
         return nullptr;
     }
-    return PyLong_FromLong((long)f(args...));
+    // Other threads run while a full launch queue holds the call up.
+    PyThreadState* state = PyEval_SaveThread();
+    const long status = (long)f(args...);
+    PyEval_RestoreThread(state);
+    return PyLong_FromLong(status);
 }
 
 template <typename T>

@@ -323,3 +323,63 @@ def test_largest_batch():
     out, lse, st = run(pool, table, lens, q, heads, page, 0.125)
     assert st == 0
     check(out, lse, pool, table, lens, q, heads, page, 0.125)
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+def test_non_finite_queries_stay_in_their_head(bad):
+    heads, group, dim, page = 2, 4, 128, 16
+    pool, table, lens, q = make([70, 5], heads, group, dim, page, seed=18)
+    clean, lse, _ = run(pool, table, lens, q, heads, page, 0.1)
+    q[0, 5, 17] = bad
+    out, lse2, st = run(pool, table, lens, q, heads, page, 0.1)
+    assert st == 0 and not bool(torch.isfinite(out[0, 5]).any())
+    keep = torch.ones(2, heads * group, dtype=torch.bool, device="cuda")
+    keep[0, 5] = False
+    assert torch.equal(out[keep], clean[keep]) and torch.equal(lse[keep], lse2[keep])
+
+
+def test_unaligned_weights():
+    """Weights that start at an odd float are added to one by one."""
+    heads, group, dim, page = 2, 3, 64, 16
+    pool, table, lens, q = make([75, 16, 3], heads, group, dim, page, seed=19)
+    n = pool.shape[0] * heads * page
+    weight0 = torch.rand(n, generator=R.gen(2)).view(pool.shape[0], heads, page)
+    room = torch.zeros(n + 2, device="cuda")
+    weight = room[1:-1].view(pool.shape[0], heads, page)
+    weight.copy_(weight0)
+    out, lse, st = run(pool, table, lens, q, heads, page, 0.1, weight=weight)
+    assert st == 0 and float(room[0]) == 0 and float(room[-1]) == 0
+    check(out, lse, pool, table, lens, q, heads, page, 0.1, weight0, weight)
+
+
+@pytest.mark.parametrize("heads,group,dim", [(1, 130, 64), (3, 33, 128)])
+def test_many_query_heads(heads, group, dim):
+    page = 32
+    pool, table, lens, q = make([90, 0, 1], heads, group, dim, page, seed=20)
+    weight0 = torch.zeros(pool.shape[0], heads, page)
+    weight = weight0.cuda()
+    out, lse, st = run(pool, table, lens, q, heads, page, 0.1, weight=weight)
+    assert st == 0
+    check(out, lse, pool, table, lens, q, heads, page, 0.1, weight0, weight)
+
+
+def test_long_context_in_large_pages():
+    """The log-sum and the total weight of a context of 70,001 equal keys have
+    closed forms; values that alternate give their mean."""
+    heads, group, dim, page, n = 1, 2, 64, 4096, 70001
+    pages = -(-n // page)
+    k = torch.full((1, heads, dim), 0.5, dtype=torch.bfloat16).expand(n, -1, -1).cuda()
+    v = torch.where(torch.arange(n) % 2 == 0, 1.0, -3.0).to(torch.bfloat16)[:, None, None].expand(-1, heads, dim).cuda()
+    pool = torch.zeros(pages, S.sz_cache_page_bytes(dim, heads, page), dtype=torch.uint8, device="cuda")
+    S.sz_cache_append(k, v, torch.arange(n, device="cuda"), pool, page)
+    table = torch.arange(pages, dtype=torch.int32)[None]
+    q = torch.full((1, heads * group, dim), 0.25, dtype=torch.bfloat16)
+    weight = torch.zeros(pages, heads, page, device="cuda")
+    out, lse, st = run(pool, table, torch.tensor([n], dtype=torch.int32), q, heads, page, 0.125, weight=weight)
+    assert st == 0
+    # What the cache holds, before any rounding of a read.
+    key, even, odd = (float(R.dequantise(*R.quantise(x.cpu()))[0]) for x in (k[0, 0], v[0, 0], v[1, 0]))
+    assert abs(float(lse[0, 0]) - (0.25 * dim * key * 0.125 + math.log(n))) < 1e-4
+    mean = (even * 35001 + odd * 35000) / n
+    assert float((out.double() - mean).abs().max()) <= 2.0 ** -7 * abs(mean) + 2.0 ** -8 * 2
+    assert abs(float(weight.double().sum()) - group) < 1e-4 and bool((weight.flatten()[n:] == 0).all())
