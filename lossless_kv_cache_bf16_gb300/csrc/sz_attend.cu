@@ -53,15 +53,23 @@ constexpr float kNegInf = -__builtin_huge_valf();
 // up to 2^26 is still finite, and a product down to 2^-85 still has all bits
 // after the factor 2^-133 of the codes.
 constexpr float kWeightShift = 92.f;
+// Entries that stand for an item's fixed cost (its queries, its results).
+// Main kernel on 64 ragged sequences up to 8,192 tokens: 32.5 us with 1, 28.0
+// with 2, 29.6 with 3.
 constexpr uint32_t kItemCost = 2;
-constexpr uint32_t kMinShare = 1;  // list entries of a warp, at least
+// List entries of a warp, at least.  One sequence of 777 tokens: 13.4 us with 4,
+// 9.9 with 2, 8.4 with 1.
+constexpr uint32_t kMinShare = 1;
 
 template <int D, int NT>
 struct Shape {
+    // As many warps as their registers allow without spilling into the loop:
+    // 168 each with 8 heads, 255 with 16.
     static constexpr int kWarps = NT == 1 ? 12 : 8;
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kHeads = 8 * NT;
     static constexpr uint32_t kUnitBytes = 2 * Cell<D>::kBytes;
+    // About 14 KB under way per warp, 166 KB per SM.
     static constexpr int kStages = (NT == 1 ? 3 : 4) * (D == 64 ? 2 : 1);
     static constexpr int kRow = D + 4;  // floats of a head's row of a piece, padded against bank conflicts
     static constexpr uint32_t kPieceBytes = 4 * kHeads * kRow + 8 * kHeads;
@@ -823,6 +831,9 @@ cudaError_t launch(const AttendParams& p, cudaStream_t s) {
 
 template <int D>
 cudaError_t launch_dim(const AttendParams& p, cudaStream_t s) {
+    // More than 8 query heads per kv head: items of 16, so that the cache is read
+    // once for all of them (12 heads, 16 sequences of 32,768 tokens: 89 us;
+    // twice 61 us with items of 8).
     if (p.group <= 8) return p.weight ? launch<D, 1, true>(p, s) : launch<D, 1, false>(p, s);
     return p.weight ? launch<D, 2, true>(p, s) : launch<D, 2, false>(p, s);
 }

@@ -428,12 +428,14 @@ cudaError_t launch_evict(const EvictParams& p, cudaStream_t s) {
     int sms = 0, per_sm = 0;
     cudaError_t err = kernel_fit(reinterpret_cast<const void*>(evict_select_kernel<0>), kThreads, 0, &sms, &per_sm);
     if (err != cudaSuccess) return err;
-    // As many blocks a list as fit on the device at once, and at least as many
-    // as hold the longest sequence's keys, 32 a thread (beyond 8 blocks the
-    // keys are read again for every pass).
+    // As many blocks a list as fit on the device at once, while a thread has more
+    // than 4 keys (8 keys a thread take 12 us in one block, 16 take 25 and 32
+    // take 47; the cluster's barriers cost 4 us, more than fewer keys than that
+    // save), and at least as many as hold the longest sequence's keys, 32 a
+    // thread (beyond 8 blocks the keys are read again for every pass).
     const uint64_t lists = (uint64_t)p.pool.heads * p.batch, longest = (uint64_t)p.table_width << p.pool.lg_page;
     uint32_t cluster = 1;
-    while (cluster < kMaxCluster && longest > (uint64_t)cluster * kThreads &&
+    while (cluster < kMaxCluster && longest > 4ull * cluster * kThreads &&
            (lists * cluster * 2 <= (uint64_t)sms || longest > 32ull * cluster * kThreads))
         cluster *= 2;
     const uint64_t keys = (longest + (uint64_t)cluster * kThreads - 1) / ((uint64_t)cluster * kThreads);
@@ -444,6 +446,8 @@ cudaError_t launch_evict(const EvictParams& p, cudaStream_t s) {
                         p, cluster, s);
     if (err != cudaSuccess) return err;
     const uint32_t blocks = (p.max_moves + 8 * kTogether - 1) / (8 * kTogether);
+    // Blocks a list: enough to take all of its moves at once in most cases.  With
+    // many lists fewer do: 128 lists' moves take 15.1 us with 16, 13.1 with 48.
     const uint32_t most = lists >= 64 ? 48 : 64;
     return launch_dependent(p.pool.dim == 64 ? evict_move_kernel<64> : evict_move_kernel<128>,
                             dim3(blocks < most ? blocks : most, p.pool.heads, p.batch), dim3(256), 0, s, p);
