@@ -47,14 +47,12 @@ bool expect(Py_ssize_t got, Py_ssize_t want) {
     return false;
 }
 
-// rows(t, bfloat16, what) -> (data_ptr, shape, stride) of a bf16 CUDA tensor
-// [rows, heads, channels] whose channels are contiguous.
-PyObject* rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    if (!expect(n, 3)) return nullptr;
-    PyObject *t = a[0], *what = a[2];
+// (data_ptr, shape, stride) of a bf16 CUDA tensor [rows, heads, channels] whose
+// channels are contiguous.
+PyObject* rows_of(PyObject* t, PyObject* bfloat16, PyObject* what) {
     Ref dtype(PyObject_GetAttr(t, s_dtype)), shape(PyObject_GetAttr(t, s_shape)), stride(PyObject_CallMethodNoArgs(t, s_stride));
     if (!dtype || !shape || !stride) return nullptr;
-    if (dtype.o != a[1] || !PyTuple_Check(shape.o) || !PyTuple_Check(stride.o) || PyTuple_GET_SIZE(shape.o) != 3 ||
+    if (dtype.o != bfloat16 || !PyTuple_Check(shape.o) || !PyTuple_Check(stride.o) || PyTuple_GET_SIZE(shape.o) != 3 ||
         PyTuple_GET_SIZE(stride.o) != 3)
         return refuse(what, "must be a bfloat16 tensor of three dimensions");
     const int cuda = truth(PyObject_GetAttr(t, s_is_cuda));
@@ -71,6 +69,47 @@ PyObject* rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Ref ptr(PyObject_CallMethodNoArgs(t, s_data_ptr));
     if (!ptr) return nullptr;
     return PyTuple_Pack(3, ptr.o, shape.o, stride.o);
+}
+
+// rows(t, bfloat16, what)
+PyObject* rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return expect(n, 3) ? rows_of(a[0], a[1], a[2]) : nullptr;
+}
+
+// written_rows(t, bfloat16, shape, what): the same for a tensor of that shape
+// which a kernel writes: no two of its rows may share memory.
+PyObject* written_rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    if (!expect(n, 4)) return nullptr;
+    PyObject* what = a[3];
+    Ref got(rows_of(a[0], a[1], what));
+    if (!got) return nullptr;
+    PyObject *shape = PyTuple_GET_ITEM(got.o, 1), *stride = PyTuple_GET_ITEM(got.o, 2);
+    const int same = PyObject_RichCompareBool(shape, a[2], Py_EQ);
+    if (same < 0) return nullptr;
+    if (!same) {
+        PyErr_Format(PyExc_ValueError, "%U must have shape %R, not %R", what, a[2], shape);
+        return nullptr;
+    }
+    // From the smallest stride on, each must reach past all that lies below.
+    long long size[3], step[3];
+    for (int k = 0; k < 3; k++) {
+        size[k] = PyLong_AsLongLong(PyTuple_GET_ITEM(shape, k));
+        step[k] = PyLong_AsLongLong(PyTuple_GET_ITEM(stride, k));
+    }
+    if (PyErr_Occurred()) return nullptr;
+    bool done[3] = {};
+    long long reach = 0;
+    for (int turn = 0; turn < 3; turn++) {
+        int next = -1;
+        for (int k = 0; k < 3; k++)
+            if (!done[k] && (next < 0 || step[k] < step[next])) next = k;
+        done[next] = true;
+        if (size[next] <= 1) continue;
+        if (step[next] <= reach) return refuse(what, "must not overlap itself");
+        reach += step[next] * (size[next] - 1);
+    }
+    Py_INCREF(got.o);
+    return got.o;
 }
 
 // pointer(t, dtype or None, count or -1, what) -> data_ptr of a contiguous CUDA
@@ -180,7 +219,7 @@ PyObject* cache_evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 #define FAST(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(name)), METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {FAST(rows),        FAST(pointer),      FAST(qk_norm_rope), FAST(cache_append),
+PyMethodDef methods[] = {FAST(rows),        FAST(written_rows), FAST(pointer),      FAST(qk_norm_rope), FAST(cache_append),
                          FAST(cache_read),  FAST(cache_attend), FAST(cache_evict),  {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_sz_bind", "Checks and calls of splitzip.py's serving operators.", -1, methods,

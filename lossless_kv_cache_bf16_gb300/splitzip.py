@@ -421,23 +421,7 @@ def sz_debug_encode_stalled(dt: int, cb, x: torch.Tensor, out: torch.Tensor, out
 # ---- serving operators around the 4-bit paged KV cache -------------------------
 
 _BF16, _F32, _I32, _I64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
-_rows, _pointer = _bind.rows, _bind.pointer
-
-
-def _written_rows(t: torch.Tensor, want, what: str):
-    """_rows of a tensor of the given shape that a kernel writes: no two of its
-    rows may share memory."""
-    ptr, shape, stride = got = _rows(t, _BF16, what)
-    if shape != want:
-        raise ValueError(f"{what} must have shape {tuple(want)}, not {tuple(shape)}")
-    if not t.is_contiguous():
-        reach = 0
-        for s, n in sorted(x for x in zip(stride, shape) if x[1] > 1):
-            if s <= reach:
-                raise ValueError(f"{what} must not overlap itself")
-            reach += s * (n - 1)
-    return got
-
+_rows, _written_rows, _pointer = _bind.rows, _bind.written_rows, _bind.pointer
 
 _PAGE_BYTES: dict = {}  # (head_dim, kv_heads, page_tokens) -> bytes of a page
 
@@ -476,8 +460,8 @@ def sz_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor | N
     tokens, q_heads, d = q_shape
     if k_shape[0] != tokens or k_shape[2] != d:
         raise ValueError("q and k must have the same tokens and head dimension")
-    qop, _, qos = _written_rows(q_out, q_shape, "q_out")
-    kop, _, kos = _written_rows(k_out, k_shape, "k_out")
+    qop, _, qos = _written_rows(q_out, _BF16, q_shape, "q_out")
+    kop, _, kos = _written_rows(k_out, _BF16, k_shape, "k_out")
     if (qp == qop and qs != qos) or (kp == kop and ks != kos):
         raise ValueError("an output over its input must have the input's strides")
     _check("sz_qk_norm_rope", _bind.qk_norm_rope(
@@ -512,8 +496,8 @@ def sz_cache_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, pool:
 def sz_cache_read(pool: torch.Tensor, page_tokens: int, slots: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
                   status: torch.Tensor | None = None, stream=None) -> None:
     """Reads the values at `slots` into k and v [tokens, kv heads, D] as bf16."""
-    kp, shape, ks = _written_rows(k, k.shape, "k")
-    vp, _, vs = _written_rows(v, shape, "v")
+    kp, shape, ks = _written_rows(k, _BF16, k.shape, "k")
+    vp, _, vs = _written_rows(v, _BF16, shape, "v")
     tokens, heads, d = shape
     _check("sz_cache_read", _bind.cache_read(
         _ADDRESS["sz_cache_read"], _pointer(pool, None, -1, "pool"), _cache_pages(pool, heads, d, page_tokens), heads, d,
@@ -536,7 +520,7 @@ def sz_cache_attend(q: torch.Tensor, pool: torch.Tensor, kv_heads: int, page_tok
     head and offset) grows by the attention weights."""
     qp, shape, qs = _rows(q, _BF16, "q")
     batch, q_heads, d = shape
-    op, _, os = _written_rows(out, shape, "out")
+    op, _, os = _written_rows(out, _BF16, shape, "out")
     if qp == op and batch:
         raise ValueError("out must not be q")
     pages = _cache_pages(pool, kv_heads, d, page_tokens)

@@ -128,7 +128,7 @@ class Recorder:
     the calls that would launch."""
 
     def __init__(self, bind):
-        self.rows, self.pointer, self.calls = bind.rows, bind.pointer, []
+        self.rows, self.written_rows, self.pointer, self.calls = bind.rows, bind.written_rows, bind.pointer, []
 
     def __getattr__(self, name):
         return lambda *a: self.calls.append(name) or 0
@@ -184,6 +184,21 @@ def test_binding_refuses_mismatched_tensors(S, monkeypatch):
         with pytest.raises(ValueError):
             f(**c)
     assert rec.calls == []
+
+
+def test_overlapping_outputs(S):
+    """Rows that share memory are told from rows that interleave."""
+    b = S._bind
+    ok = [fake(4, 2, 64), fake(2, 4, 64).transpose(0, 1), fake(4, 6, 64)[:, 2:4], fake(4, 2, 70)[..., :64],
+          fake(1, 1, 64).expand(1, 1, 64), fake(0, 2, 64), fake(4, 1, 64)[:, :1]]
+    for t in ok:
+        assert b.written_rows(t, torch.bfloat16, t.shape, "t")[1:] == (t.shape, t.stride())
+    for t in (fake(1, 2, 64).expand(4, 2, 64), fake(4, 1, 64).expand(4, 2, 64), fake(600).as_strided((4, 2, 64), (64, 32, 1)),
+              fake(600).as_strided((4, 2, 64), (64, 64, 1)), fake(600).as_strided((2, 4, 64), (100, 64, 1))):
+        with pytest.raises(ValueError, match="overlap"):
+            b.written_rows(t, torch.bfloat16, t.shape, "t")
+    with pytest.raises(ValueError, match="shape"):
+        b.written_rows(ok[0], torch.bfloat16, (4, 2, 32), "t")
 
 
 def test_bad_values_do_not_reach_the_library(S):
