@@ -30,7 +30,8 @@
 // else: it has its own ring of bulk copies, its own running maximum and sums,
 // and writes the rows of an item that it holds whole.  Pieces of an item are
 // joined once per block in shared memory, pieces over several blocks by a
-// second kernel, both in list order: results do not depend on timing.
+// second kernel, both in list order: results do not depend on timing.  Few
+// short sequences take one block per item and no second kernel (launch()).
 //
 // Measured: each 8 sequences of 32,768 tokens more (4 kv heads of 128, 28
 // query heads, 151 MB) take 26 us, 5.7 TB/s or 85% of the copy rate, after
@@ -57,8 +58,8 @@ constexpr float kWeightShift = 92.f;
 // Main kernel on 64 ragged sequences up to 8,192 tokens: 32.5 us with 1, 28.0
 // with 2, 29.6 with 3.
 constexpr uint32_t kItemCost = 2;
-// List entries of a warp, at least.  One sequence of 777 tokens: 13.4 us with 4,
-// 9.9 with 2, 8.4 with 1.
+// List entries of a warp, at least.  One sequence of 777 tokens cut into runs:
+// 13.4 us with 4, 9.9 with 2, 8.4 with 1 (main kernel).
 constexpr uint32_t kMinShare = 1;
 
 template <int D, int NT>
@@ -223,7 +224,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attend_kernel(const
     const uint64_t workers = (uint64_t)gridDim.x * W;
     const uint32_t share = (uint32_t)max(divide(total + workers - 1, workers), (uint64_t)kMinShare);
     const uint64_t u0 = min(((uint64_t)blockIdx.x * W + warp) * share, total);
-    const uint32_t n_run = (uint32_t)(min(u0 + share, total) - u0);
+    uint32_t n_run = (uint32_t)(min(u0 + share, total) - u0);
     // Rows of empty sequences are zero, with a log-sum of -infinity.
     for (uint32_t b = blockIdx.x; b < p.batch; b += gridDim.x) {
         if (s_len[b]) continue;
@@ -234,9 +235,17 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attend_kernel(const
     }
     if (tid == 0) p.meta[4 * blockIdx.x] = -1;
 
-    // ---- where this warp's run starts: the lengths, 32 at a time ----
+    // ---- where this warp's run starts ----
     Cursor cur{0, 0, 0};
-    if (n_run) {
+    if (p.whole_items) {
+        // One item a block: its units in equal runs.
+        cur.b = blockIdx.x / items, cur.item = blockIdx.x % items;
+        const uint32_t units = (s_len[cur.b] + kUnitTokens - 1) / kUnitTokens, per = (units + W - 1) / W;
+        const uint32_t from = min(warp * per, units);
+        cur.at = kItemCost + from;
+        n_run = min(per, units - from);
+    } else if (n_run) {
+        // The lengths, 32 at a time.
         uint64_t before = 0;
         for (uint32_t b0 = 0; b0 < p.batch; b0 += 32) {
             const uint32_t n = b0 + lane < p.batch ? entries(s_len[b0 + lane]) : 0u;
@@ -820,11 +829,22 @@ cudaError_t launch(const AttendParams& p, cudaStream_t s) {
     int sms = 0, per_sm = 0;
     cudaError_t err = kernel_fit(reinterpret_cast<const void*>(attend_kernel<D, NT, LOGITS>), Sh::kThreads, Sh::kBytes, &sms, &per_sm);
     if (err != cudaSuccess) return err;
-    err = launch_dependent(attend_kernel<D, NT, LOGITS>, dim3((uint32_t)sms), dim3(Sh::kThreads), Sh::kBytes, s, p);
-    if (err != cudaSuccess) return err;
-    err = launch_dependent(attend_join_kernel<D>, dim3((uint32_t)sms), dim3(256), 0, s, p, (uint32_t)Sh::kHeads);
-    if (err != cudaSuccess || !LOGITS) return err;
     const uint64_t tokens = (uint64_t)p.table_width << p.pool.lg_page;
+    // No more items than SMs, and a table with room for only 3 units a warp:
+    // one item a block, and no join across blocks to launch.  With 8 items
+    // (32 heads over 8 of 128 channels) of 384 tokens 7.5 us against 10.4 in
+    // runs, of 768 tokens 8.9 against 10.4, of 1,152 (3 units a warp) 10.1
+    // against 10.1; of 1,536 11.8 against 10.5, but 12.0 against 15.2 with 128
+    // items, so that far only where the items fill half the SMs.
+    const uint64_t items = (uint64_t)p.batch * p.pool.heads * p.tiles;
+    const uint64_t unit_a_warp = (uint64_t)Sh::kWarps * kUnitTokens;
+    AttendParams q = p;
+    q.whole_items = items <= (uint64_t)sms && tokens <= (2 * items >= (uint64_t)sms ? 4 : 3) * unit_a_warp;
+    err = launch_dependent(attend_kernel<D, NT, LOGITS>, dim3(q.whole_items ? (uint32_t)items : (uint32_t)sms), dim3(Sh::kThreads),
+                           Sh::kBytes, s, q);
+    if (err != cudaSuccess) return err;
+    if (!q.whole_items) err = launch_dependent(attend_join_kernel<D>, dim3((uint32_t)sms), dim3(256), 0, s, p, (uint32_t)Sh::kHeads);
+    if (err != cudaSuccess || !LOGITS) return err;
     const uint32_t blocks = (uint32_t)((tokens + 1023) / 1024);
     return launch_dependent(attend_weight_kernel, dim3(blocks < 1024 ? blocks : 1024, p.pool.heads, p.batch), dim3(256), 0, s, p);
 }

@@ -68,6 +68,7 @@ struct AttendParams {
     float* weight;     // nullable
     int* status;       // nullable
     uint64_t wait_limit_ns;
+    int whole_items;  // one item a block (set by the launch)
     int q_vec, out_vec, weight_vec;  // query rows are 16-byte, output rows 8-byte, weights 16-byte aligned
     // workspace
     int32_t* meta;   // [blocks][4]

@@ -383,3 +383,35 @@ def test_long_context_in_large_pages():
     mean = (even * 35001 + odd * 35000) / n
     assert float((out.double() - mean).abs().max()) <= 2.0 ** -7 * abs(mean) + 2.0 ** -8 * 2
     assert abs(float(weight.double().sum()) - group) < 1e-4 and bool((weight.flatten()[n:] == 0).all())
+
+
+@pytest.mark.parametrize("weighted", [False, True])
+@pytest.mark.parametrize("page", [16, 64, 1024])
+def test_short_contexts_in_a_wide_table(page, weighted):
+    """The same lengths with room for 8,192 tokens in the table: their items
+    are dealt out to warps in runs instead of one to a block."""
+    heads, group, dim = 2, 4, 128
+    sizes = [0, 1, 2, 15, 16, 17, 31, 32, 33, 0, 47, 48, 49, 63, 64, 65, 127, 128, 129, 0]
+    pool, table, lens, q = make(sizes, heads, group, dim, page, seed=page + 1)
+    narrow, lse0, _ = run(pool, table, lens, q, heads, page, 0.09)
+    table = torch.cat((table, torch.full((len(sizes), 8192 // page - table.shape[1]), -1, dtype=torch.int32)), 1)
+    weight0 = torch.rand(pool.shape[0], heads, page, generator=R.gen(1))
+    weight = weight0.cuda() if weighted else None
+    out, lse, st = run(pool, table, lens, q, heads, page, 0.09, weight=weight)
+    assert st == 0
+    check(out, lse, pool, table, lens, q, heads, page, 0.09, weight0, weight)
+    check(narrow, lse0, pool, table, lens, q, heads, page, 0.09)
+
+
+@pytest.mark.parametrize("tokens", [1, 383, 384, 385, 767, 768, 1152, 1535, 1536])
+@pytest.mark.parametrize("heads,group", [(1, 8), (40, 1), (8, 9), (2, 20)])
+def test_items_of_their_own_blocks(tokens, heads, group):
+    """Lengths around the units that a block's warps share out, up to and past
+    the widest table that takes this way."""
+    dim, page = 64, 128
+    n, width = tokens, -(-tokens // page)
+    pool, table, lens, q = make([n, max(0, n - 37)], heads, group, dim, page, seed=tokens + heads)
+    table = torch.cat((table, torch.full((2, width - table.shape[1]), -1, dtype=torch.int32)), 1)
+    out, lse, st = run(pool, table, lens, q, heads, page, 0.125)
+    assert st == 0
+    check(out, lse, pool, table, lens, q, heads, page, 0.125)
