@@ -15,10 +15,12 @@
 // largest (11, 11 and 10 bits), then three passes in slot order: ties that
 // survive, holes and movers are counted, then numbered.  The blocks of a
 // cluster join their histograms and counts through each other's shared
-// memory.  Second kernel: the moves, four at a time to a warp.  Both are
-// bound by latency: 8 bytes a slot are read, and few tokens move (8 sequences
-// of 32,768 tokens, 4 heads, cut by a page: 18 us for the selection, 5 us for
-// the moves, against 1.3 us for their bytes).
+// memory.  Second kernel: the moves, eight lanes each.  Both are bound by
+// latency: 8 bytes a slot are read, and few tokens move (8 sequences of 32,768
+// tokens, 4 heads, cut by a page: 17 us for the selection, 4 us for the moves,
+// against 1.3 us for their bytes).
+#include <type_traits>
+
 #include "sz_cache.cuh"
 #include "sz_params.h"
 
@@ -348,62 +350,116 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictPa
     if (blocks > 1) cluster_sync();  // no block leaves while another reads its counts
 }
 
-constexpr uint32_t kTogether = 4;  // moves of a warp at a time
+constexpr uint32_t kTogether = 4;  // moves of a warp at a time, 8 lanes each
+constexpr uint32_t kMoveThreads = 128;
 
+// The lists' moves in groups of up to kTogether, one list after the other, in
+// equal runs to the warps: few lists may have all the moves.  About 30,000
+// moves in 16 of 128 lists take 7.5 us; with blocks set aside for each list
+// and a move's words spread over a whole warp they took 12.7, with blocks of
+// 256 threads 7.9, of 512 9.1.
 template <int D>
-__global__ void __launch_bounds__(256) evict_move_kernel(const EvictParams p) {
+__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictParams p) {
     using C = Cell<D>;
+    constexpr uint32_t kSegments = kMoveThreads;
+    __shared__ uint32_t s_start[kSegments];  // groups before segment s of the lists
+    __shared__ uint32_t s_moves[kSegments];  // of its list, in segments of one list
+    __shared__ uint32_t s_warp[kMoveThreads / 32];
     wait_for_previous();
-    const uint32_t lane = threadIdx.x & 31u;
-    const Slots slots{p, blockIdx.z, blockIdx.y};
-    const uint32_t list = blockIdx.z * p.pool.heads + blockIdx.y;
-    const uint32_t n = p.moves[list];
-    const uint32_t* to_list = p.pairs + 2ull * list * p.max_moves;
-    // Lane l: K and V word l (of D / 4), and a scale word in the first D / 16 lanes.
-    const uint32_t i = lane / 8, r = lane % 8, j = lane % (D / 32);
-    const uint32_t value = lane < D / 32 ? 0 : D / 2;
-    for (uint32_t k0 = (blockIdx.x * 8 + threadIdx.x / 32) * kTogether; k0 < n; k0 += gridDim.x * 8 * kTogether) {
-        // Entry of the tables, target in lanes 0 .. 3 and source in lanes 4 .. 7.
-        uint64_t at = 0;
-        bool good = false;
-        if (lane < 2 * kTogether && k0 + lane % kTogether < n)
-            good = slots.find(to_list[(lane < kTogether ? 0 : p.max_moves) + k0 + lane % kTogether], at);
-        const uint32_t mask = __ballot_sync(0xFFFFFFFFu, good);
-        uint16_t v[kTogether][3];
-        uint16_t* target[kTogether];
-        uint32_t tok[kTogether];
-        float weight[kTogether];
-        int32_t pos[kTogether];
-        uint64_t entry[kTogether];
+    const uint32_t tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    const uint32_t lists = p.batch * p.pool.heads, segment = (lists + kSegments - 1) / kSegments;
+    auto moves = [&](uint32_t list) { return list < lists ? p.moves[list] : 0u; };
+    auto groups = [](uint32_t n) { return (n + kTogether - 1) / kTogether; };
+    auto scan = [&](uint32_t v) {  // inclusive, over the warp
 #pragma unroll
-        for (uint32_t e = 0; e < kTogether; e++) {
-            entry[e] = __shfl_sync(0xFFFFFFFFu, at, e);
-            const uint64_t from = __shfl_sync(0xFFFFFFFFu, at, kTogether + e);
-            target[e] = nullptr;
-            if ((mask >> e & mask >> (kTogether + e) & 1u) == 0) continue;
-            target[e] = reinterpret_cast<uint16_t*>(p.pool.base + (entry[e] >> 4) * C::kBytes);
-            tok[e] = (uint32_t)entry[e] & 15u;
-            const uint16_t* cell = reinterpret_cast<const uint16_t*>(p.pool.base + (from >> 4) * C::kBytes);
-            const uint32_t t = (uint32_t)from & 15u;
-            if (lane < D / 4) {
-                v[e][0] = cell[C::k_word(t, i, r)];
-                v[e][1] = cell[C::v_word(t, i, r)];
-            }
-            if (lane < D / 16) v[e][2] = cell[C::scale_word(t, j) + value];
-            if (lane == 0) weight[e] = p.weight[from];
-            if (lane == 1) pos[e] = p.pos[from];
+        for (int d = 1; d < 32; d *= 2) {
+            const uint32_t o = __shfl_up_sync(0xFFFFFFFFu, v, d);
+            if (lane >= (uint32_t)d) v += o;
         }
+        return v;
+    };
+    uint32_t own = 0, last = 0;
+    for (uint32_t e = 0; e < segment; e++) own += groups(last = moves(tid * segment + e));
+    uint32_t upto = scan(own);
+    if (lane == 31) s_warp[warp] = upto;
+    __syncthreads();
+    uint32_t total = 0;
 #pragma unroll
-        for (uint32_t e = 0; e < kTogether; e++) {
-            if (!target[e]) continue;
-            if (lane < D / 4) {
-                target[e][C::k_word(tok[e], i, r)] = v[e][0];
-                target[e][C::v_word(tok[e], i, r)] = v[e][1];
+    for (uint32_t w = 0; w < kMoveThreads / 32; w++) {
+        if (w < warp) upto += s_warp[w];
+        total += s_warp[w];
+    }
+    s_start[tid] = upto - own;
+    s_moves[tid] = segment == 1 ? last : 0u;
+    __syncthreads();
+
+    // This warp's run, and the last segment that starts at or before it.
+    const uint32_t workers = gridDim.x * (kMoveThreads / 32), share = (total + workers - 1) / workers;
+    const uint64_t first = (uint64_t)(blockIdx.x * (kMoveThreads / 32) + warp) * share;
+    if (first >= total) return;
+    uint32_t left = min(share, total - (uint32_t)first);
+    uint32_t at_or_before = 0;
+#pragma unroll
+    for (uint32_t e = 0; e < kSegments / 32; e++) at_or_before += s_start[lane + 32 * e] <= (uint32_t)first;
+    const uint32_t seg = __reduce_add_sync(0xFFFFFFFFu, at_or_before) - 1;
+    uint32_t list = seg * segment, group = (uint32_t)first - s_start[seg], n = s_moves[seg];
+    // Eight lanes a move.  Lane q of them has an eighth of K's bytes, which are
+    // in a row; row q of V, a word for each 32 channels next to the word of the
+    // token's even or odd neighbour (loaded with it, stored alone); a scale
+    // word in the first D / 16; and the weight or the position.
+    constexpr uint32_t kGroups = D / 32;
+    using KPart = std::conditional_t<D == 128, uint2, uint32_t>;
+    struct alignas(4 * kGroups) VPart {
+        uint32_t pair[kGroups];
+    };
+    const uint32_t e = lane / 8, q = lane % 8;
+    for (; left; left--, group++) {
+        while (group * kTogether >= n) {  // on to the list that holds the group, 32 at a time
+            group -= groups(n);
+            list += n ? 1 : 0;
+            n = 0;
+            if (list >= lists) return;
+            const uint32_t count = moves(list + lane), here = groups(count), sum = scan(here);
+            const uint32_t holds = __ballot_sync(0xFFFFFFFFu, sum > group);
+            if (!holds) {
+                group -= __shfl_sync(0xFFFFFFFFu, sum, 31);
+                list += 32;
+                continue;
             }
-            if (lane < D / 16) target[e][C::scale_word(tok[e], j) + value] = v[e][2];
-            if (lane == 0) p.weight[entry[e]] = weight[e];
-            if (lane == 1) p.pos[entry[e]] = pos[e];
+            const uint32_t to = __ffs(holds) - 1;
+            group -= __shfl_sync(0xFFFFFFFFu, sum - here, to);
+            list += to;
+            n = __shfl_sync(0xFFFFFFFFu, count, to);
         }
+        const Slots slots{p, list / p.pool.heads, list % p.pool.heads};
+        const uint32_t* to_list = p.pairs + 2ull * list * p.max_moves;
+        const uint32_t k = group * kTogether + e;
+        uint64_t to = 0, from = 0;
+        bool good = k < n;
+        const uint32_t target_slot = good ? to_list[k] : 0u, source_slot = good ? to_list[p.max_moves + k] : 0u;
+        good &= slots.find(target_slot, to);
+        good &= slots.find(source_slot, from);
+        if (!good) continue;
+        const uint8_t* source = p.pool.base + (from >> 4) * C::kBytes;
+        uint8_t* target = p.pool.base + (to >> 4) * C::kBytes;
+        const uint16_t* source_word = reinterpret_cast<const uint16_t*>(source);
+        uint16_t* target_word = reinterpret_cast<uint16_t*>(target);
+        const uint32_t st = (uint32_t)from & 15u, tt = (uint32_t)to & 15u;
+        const uint32_t scale = q % kGroups, value = q < kGroups ? 0 : D / 2;
+        const KPart k_part = reinterpret_cast<const KPart*>(source_word + C::k_word(st, 0, 0))[q];
+        const VPart v_part = *reinterpret_cast<const VPart*>(source_word + C::v_word(st & ~1u, 0, q));
+        uint16_t scale_word = 0;
+        float weight = 0.f;
+        int32_t pos = 0;
+        if (q < 2 * kGroups) scale_word = source_word[C::scale_word(st, scale) + value];
+        if (q == 0) weight = p.weight[from];
+        if (q == 1) pos = p.pos[from];
+        reinterpret_cast<KPart*>(target_word + C::k_word(tt, 0, 0))[q] = k_part;
+#pragma unroll
+        for (uint32_t i = 0; i < kGroups; i++) target_word[C::v_word(tt, i, q)] = (uint16_t)(v_part.pair[i] >> 16 * (st & 1u));
+        if (q < 2 * kGroups) target_word[C::scale_word(tt, scale) + value] = scale_word;
+        if (q == 0) p.weight[to] = weight;
+        if (q == 1) p.pos[to] = pos;
     }
 }
 
@@ -445,12 +501,12 @@ cudaError_t launch_evict(const EvictParams& p, cudaStream_t s) {
                                      : evict_select_kernel<0>,
                         p, cluster, s);
     if (err != cudaSuccess) return err;
-    const uint32_t blocks = (p.max_moves + 8 * kTogether - 1) / (8 * kTogether);
-    // Blocks a list: enough to take all of its moves at once in most cases.  With
-    // many lists fewer do: 128 lists' moves take 15.1 us with 16, 13.1 with 48.
-    const uint32_t most = lists >= 64 ? 48 : 64;
-    return launch_dependent(p.pool.dim == 64 ? evict_move_kernel<64> : evict_move_kernel<128>,
-                            dim3(blocks < most ? blocks : most, p.pool.heads, p.batch), dim3(256), 0, s, p);
+    void (*move)(EvictParams) = p.pool.dim == 64 ? evict_move_kernel<64> : evict_move_kernel<128>;
+    err = kernel_fit(reinterpret_cast<const void*>(move), kMoveThreads, 0, &sms, &per_sm);
+    if (err != cudaSuccess) return err;
+    constexpr uint32_t per_block = kMoveThreads / 32 * kTogether;
+    const uint64_t blocks = (lists * p.max_moves + per_block - 1) / per_block, most = (uint64_t)sms * per_sm;
+    return launch_dependent(move, dim3((uint32_t)(blocks < most ? blocks : most)), dim3(kMoveThreads), 0, s, p);
 }
 
 }  // namespace sz

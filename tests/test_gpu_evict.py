@@ -194,3 +194,25 @@ def test_graph_replay():
         graph.replay()
         torch.cuda.synchronize()
         same([x.cpu() for x in dev[:3]] + [new.cpu()], reference(pool, table, n, weight, pos, n, heads, dim, page, 32, 4))
+
+
+@pytest.mark.parametrize("batch,heads", [(128, 1), (43, 3), (70, 7), (400, 1)])
+@pytest.mark.parametrize("spread", ["all", "few", "one", "none"])
+def test_many_lists(batch, heads, spread):
+    """More (sequence, head) pairs than threads that count their moves; moves
+    in all of them, in runs with gaps, only in the last sequence, nowhere."""
+    dim, page, keep, recent = 64, 16, 24, 5
+    g = R.gen(batch + heads)
+    n = torch.randint(0, 25, (batch,), generator=g)
+    if spread == "all":
+        n += 25
+    elif spread == "few":
+        n[::37] = 70
+    elif spread == "one":
+        n[-1] = 900
+    lens = n.tolist()
+    pool, table, lens, weight, pos = make(lens, heads, dim, page, seed=batch)
+    next_pos = lens.clone()
+    got, st = run(pool, table, lens, weight, pos, next_pos, heads, dim, page, keep, recent)
+    assert st == 0
+    same(got, reference(pool, table, lens, weight, pos, next_pos, heads, dim, page, keep, recent))
