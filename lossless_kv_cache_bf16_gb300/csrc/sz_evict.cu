@@ -17,7 +17,7 @@
 // cluster join their histograms and counts through each other's shared
 // memory.  Second kernel: the moves, eight lanes each.  Both are bound by
 // latency: 8 bytes a slot are read, and few tokens move (8 sequences of 32,768
-// tokens, 4 heads, cut by a page: 17 us for the selection, 4 us for the moves,
+// tokens, 4 heads, cut by a page: 14 us for the selection, 4 us for the moves,
 // against 1.3 us for their bytes).
 #include <type_traits>
 
@@ -48,21 +48,27 @@ __device__ __forceinline__ uint32_t cluster_size() {
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// A word of this block's shared memory as block `rank` of the cluster holds it.
-__device__ __forceinline__ uint32_t peer_word(const uint32_t* p, uint32_t rank) {
-    uint32_t a, v;
+// Two words of this block's shared memory (8-byte aligned) as block `rank` of
+// the cluster holds them.
+__device__ __forceinline__ uint2 peer_pair(const uint32_t* p, uint32_t rank) {
+    uint32_t a;
+    uint2 v;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
     return v;
 }
 
-// Its sum over the first n blocks, with the loads under way together.
-__device__ __forceinline__ uint32_t peer_sum(const uint32_t* p, uint32_t n) {
-    uint32_t v[kMaxCluster], sum = 0;
+// Their sums over the cluster's n blocks, with the loads under way together;
+// `before`, if given: over the first `rank` of them.
+__device__ __forceinline__ uint2 peer_sums(const uint32_t* p, uint32_t n, uint32_t rank = 0, uint2* before = nullptr) {
+    uint2 v[kMaxCluster], sum{0, 0};
 #pragma unroll
-    for (uint32_t r = 0; r < kMaxCluster; r++) v[r] = r < n ? peer_word(p, r) : 0u;
+    for (uint32_t r = 0; r < kMaxCluster; r++) v[r] = r < n ? peer_pair(p, r) : uint2{0, 0};
 #pragma unroll
-    for (uint32_t r = 0; r < kMaxCluster; r++) sum += v[r];
+    for (uint32_t r = 0; r < kMaxCluster; r++) {
+        if (before && r == rank) *before = sum;
+        sum.x += v[r].x, sum.y += v[r].y;
+    }
     return sum;
 }
 
@@ -120,17 +126,17 @@ struct Slots {
 // again for every pass.
 template <int KEYS>
 __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictParams p) {
-    __shared__ uint32_t s_bins[kCopies * kBins];
+    __shared__ alignas(8) uint32_t s_bins[kCopies * kBins];
     __shared__ uint32_t s_count[2][kWarps];
-    __shared__ uint32_t s_sum[2][2];  // of the block: ties; holes and movers
-    __shared__ uint32_t s_safe;       // the block's protected tokens
+    __shared__ alignas(8) uint32_t s_sum[2][2];  // of the block: ties; holes and movers
+    __shared__ alignas(8) uint32_t s_safe[2];    // the block's protected tokens (and 0)
     __shared__ uint32_t s_pick[3];  // a bin, how many of its keys survive, how many it has
     wait_for_previous();
     const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31u;
     const uint32_t rank = cluster_rank(), blocks = cluster_size();
     const Slots slots{p, blockIdx.z, blockIdx.y};
     const uint32_t list = blockIdx.z * p.pool.heads + blockIdx.y;
-    const int32_t len = p.lens[slots.b];
+    const int32_t len = p.lens[slots.b], next_pos = p.next_pos[slots.b];
     const bool ok = len >= 0 && (uint64_t)len <= (uint64_t)p.table_width << p.pool.lg_page;
     const uint32_t n = ok ? (uint32_t)len : 0u;
     if (tid == 0 && rank == 0) {
@@ -139,7 +145,7 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictPa
         if (n <= p.keep) p.moves[list] = 0;
     }
     if (n <= p.keep) return;  // the whole cluster
-    const int64_t safe_from = (int64_t)p.next_pos[slots.b] - (int64_t)p.recent;
+    const int64_t safe_from = (int64_t)next_pos - (int64_t)p.recent;
 
     // This warp's slots [from, to), in order of block and warp.
     const uint32_t runs = blocks * kWarps;
@@ -189,9 +195,9 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictPa
         }
         if (tid == 0) s_sum[k][0] = all_x, s_sum[k][1] = all_y;
         cluster_sync();
-        x += peer_sum(&s_sum[k][0], rank);
-        y += peer_sum(&s_sum[k][1], rank);
-        all_x = peer_sum(&s_sum[k][0], blocks);
+        uint2 before{0, 0};
+        all_x = peer_sums(s_sum[k], blocks, rank, &before).x;
+        x += before.x, y += before.y;
         return all_x;
     };
 
@@ -208,45 +214,68 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictPa
         const uint32_t width = level == 2 ? 1024 : 2048;
         uint32_t* own = s_bins + level * kBins;
         for (uint32_t i = tid; i < (level == 0 ? kCopies : 1) * kBins; i += kThreads) own[i] = 0;
-        if (level == 0 && tid == 0) s_safe = 0;
+        if (level == 0 && tid < 2) s_safe[tid] = 0;
         __syncthreads();
         uint32_t* bins = own + (level == 0 ? lane % kCopies * kBins : 0);
         uint32_t safe = 0;
-        if (level == 0) each([&](uint32_t, uint32_t k, bool in) { safe += in && k == kProtected; });
-        each([&](uint32_t, uint32_t k, bool in) {
-            in = in && k != apart && (k & fixed) == threshold;
-            if (!__any_sync(0xFFFFFFFFu, in)) return;
-            const uint32_t bin = (k >> shift) & (width - 1);
-            // A warp whose keys share a bin (equal weights) adds once.
-            const uint32_t who = __ballot_sync(0xFFFFFFFFu, in);
-            const uint32_t lead = __ffs(who) - 1;
-            const uint32_t bin0 = __shfl_sync(0xFFFFFFFFu, bin, lead);
-            if (__all_sync(0xFFFFFFFFu, !in || bin == bin0)) {
-                if (lane == lead) atomicAdd(&own[bin0], __popc(who));
-            } else if (in) {
-                atomicAdd(&bins[bin], 1u);
+        // N keys of a lane, 32 slots apart.  A warp whose keys all share a bin
+        // (equal weights) adds once.
+        auto tally = [&](auto n_keys, const uint32_t* k, uint32_t i0) {
+            constexpr int N = decltype(n_keys)::value;
+            uint32_t every = 0xFFFFFFFFu, some = 0, count = 0, bin[N];
+#pragma unroll
+            for (int j = 0; j < N; j++) {
+                bool in = i0 + 32 * j + lane < to;
+                if (level == 0) safe += in && k[j] == kProtected;
+                in = in && k[j] != apart && (k[j] & fixed) == threshold;
+                bin[j] = in ? (k[j] >> shift) & (width - 1) : 0xFFFFFFFFu;
+                every &= bin[j], some |= in ? bin[j] : 0u, count += in;
             }
-        });
+            every = __reduce_and_sync(0xFFFFFFFFu, every);
+            some = __reduce_or_sync(0xFFFFFFFFu, some);
+            if (every == some) {
+                count = __reduce_add_sync(0xFFFFFFFFu, count);
+                if (lane == 0) atomicAdd(&own[some], count);
+            } else if (count) {
+#pragma unroll
+                for (int j = 0; j < N; j++)
+                    if (bin[j] != 0xFFFFFFFFu) atomicAdd(&bins[bin[j]], 1u);
+            }
+        };
+        if constexpr (KEYS > 0) {
+            constexpr int kBatch = KEYS < 8 ? KEYS : 8;
+#pragma unroll
+            for (int j = 0; j < KEYS; j += kBatch) tally(std::integral_constant<int, kBatch>{}, keys + j, from + 32 * j);
+        } else {
+            each([&](uint32_t i, uint32_t k, bool) { tally(std::integral_constant<int, 1>{}, &k, i - lane); });
+        }
         if (level == 0) {
             safe = __reduce_add_sync(0xFFFFFFFFu, safe);
-            if (lane == 0 && safe) atomicAdd(&s_safe, safe);
+            if (lane == 0 && safe) atomicAdd(s_safe, safe);
         }
         __syncthreads();
+        // The counts of two neighbouring bins: thread t has bins 2 t and 2 t + 1
+        // from the top, of all blocks.
+        const uint32_t pair = 2 * tid < width ? width - 2 - 2 * tid : 0u;
+        uint2 two = *reinterpret_cast<const uint2*>(&own[pair]);
         if (level == 0) {
-            for (uint32_t i = tid; i < kBins; i += kThreads) {
-                uint32_t sum = 0;
-                for (uint32_t c = 0; c < kCopies; c++) sum += own[c * kBins + i];
-                own[i] = sum;
+#pragma unroll
+            for (uint32_t c = 1; c < kCopies; c++) {
+                const uint2 o = *reinterpret_cast<const uint2*>(&own[c * kBins + pair]);
+                two.x += o.x, two.y += o.y;
             }
         }
-        if (blocks > 1)
+        uint32_t all_safe = s_safe[0];
+        if (blocks > 1) {
+            if (level == 0) *reinterpret_cast<uint2*>(&own[pair]) = two;
             cluster_sync();
-        else
-            __syncthreads();
+            two = peer_sums(&own[pair], blocks);
+            if (level == 0) all_safe = peer_sums(s_safe, blocks).x;
+        }
+        if (2 * tid >= width) two = uint2{0, 0};
         if (level == 0 && !only_safe) {
-            safe = peer_sum(&s_safe, blocks);
-            need = p.keep - safe;
-            if (safe >= p.keep) {
+            need = p.keep - all_safe;
+            if (all_safe >= p.keep) {
                 // The protected tokens are enough: they compete, and no other
                 // stays.  Once more from the start.
                 only_safe = true;
@@ -261,17 +290,8 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictPa
                 continue;
             }
         }
-        // The bin that holds the need-th largest.  Thread t has bins 2 t and
-        // 2 t + 1 from the top, of all blocks.
-        uint32_t two[2] = {0, 0};
-        if (2 * tid < width) {
-#pragma unroll
-            for (int e = 0; e < 2; e++) {
-                const uint32_t* bin = &own[width - 1 - 2 * tid - e];
-                two[e] = blocks == 1 ? *bin : peer_sum(bin, blocks);
-            }
-        }
-        uint32_t upto = two[0] + two[1];
+        // The bin that holds the need-th largest.
+        uint32_t upto = two.y + two.x;
 #pragma unroll
         for (int d = 1; d < 32; d *= 2) {
             const uint32_t o = __shfl_up_sync(0xFFFFFFFFu, upto, d);
@@ -281,12 +301,12 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictPa
         __syncthreads();
         const uint32_t others = s_count[0][lane];
         upto += __reduce_add_sync(0xFFFFFFFFu, lane < warp ? others : 0u);
-        const uint32_t past = upto - two[0] - two[1];  // in higher bins
+        const uint32_t past = upto - two.y - two.x;  // in higher bins
         if (past < need && need <= upto) {
-            const bool second = need > past + two[0];
+            const bool second = need > past + two.y;
             s_pick[0] = width - 1 - 2 * tid - (second ? 1u : 0u);
-            s_pick[1] = need - past - (second ? two[0] : 0u);
-            s_pick[2] = second ? two[1] : two[0];
+            s_pick[1] = need - past - (second ? two.y : 0u);
+            s_pick[2] = second ? two.x : two.y;
         }
         __syncthreads();
         threshold |= s_pick[0] << shift;
@@ -306,26 +326,27 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictPa
         each([&](uint32_t, uint32_t k, bool in) { ties_before += __popc(__ballot_sync(0xFFFFFFFFu, in && k == threshold)); });
         place(ties_before, none, 0);
     }
-    // What becomes of this lane's slots, a bit each (KEYS of them), or found
-    // again for the second pass.
-    uint32_t hole_bits = 0, mover_bits = 0, hole = 0, mover = 0, tie = ties_before;
-    auto sort_out = [&](uint32_t i, uint32_t k, bool in, uint32_t& hb, uint32_t& mb) {
-        bool stays = in && k >= threshold;
+    // Whether a slot's token stays, for the slots in order.
+    uint32_t tie = ties_before;
+    auto stays = [&](uint32_t k, bool in) {
+        bool yes = in && k >= threshold;
         if (!all_pass) {
             const uint32_t eq = __ballot_sync(0xFFFFFFFFu, in && k == threshold);
-            stays = stays && (k != threshold || tie + __popc(eq & below) < need);
+            yes = yes && (k != threshold || tie + __popc(eq & below) < need);
             tie += __popc(eq);
         }
-        hb = __ballot_sync(0xFFFFFFFFu, in && i < p.keep && !stays);
-        mb = __ballot_sync(0xFFFFFFFFu, i >= p.keep && stays);
+        return yes;
     };
-    uint32_t bit = 0;
+    // The lane's holes and movers: counted, and kept a bit each (KEYS of them) or
+    // found again for the second pass.
+    uint32_t moving = 0, bit = 0, hole = 0, mover = 0;
     each([&](uint32_t i, uint32_t k, bool in) {
-        uint32_t hb, mb;
-        sort_out(i, k, in, hb, mb);
-        hole += __popc(hb), mover += __popc(mb);
-        if constexpr (KEYS > 0) hole_bits |= (hb >> lane & 1u) << bit, mover_bits |= (mb >> lane & 1u) << bit, bit++;
+        const bool yes = stays(k, in), is_hole = in && i < p.keep && !yes, is_mover = i >= p.keep && yes;
+        hole += is_hole, mover += is_mover;
+        if constexpr (KEYS > 0) moving |= (uint32_t)(is_hole || is_mover) << bit++;
     });
+    hole = __reduce_add_sync(0xFFFFFFFFu, hole);
+    mover = __reduce_add_sync(0xFFFFFFFFu, mover);
     const uint32_t holes = place(hole, mover, 1);
     if (tid == 0 && rank == 0) p.moves[list] = min(holes, p.max_moves);
     uint32_t* to_list = p.pairs + 2ull * list * p.max_moves;
@@ -333,19 +354,21 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictPa
     bit = 0;
     tie = ties_before;
     each([&](uint32_t i, uint32_t k, bool in) {
-        uint32_t hb, mb;
+        bool moves;
         if constexpr (KEYS > 0) {
-            hb = __ballot_sync(0xFFFFFFFFu, hole_bits >> bit & 1u);
-            mb = __ballot_sync(0xFFFFFFFFu, mover_bits >> bit & 1u);
-            bit++;
+            moves = moving >> bit++ & 1u;
         } else {
-            sort_out(i, k, in, hb, mb);
+            const bool yes = stays(k, in);
+            moves = in && (i < p.keep) != yes;
         }
-        const uint32_t hi = hole + __popc(hb & below), mi = mover + __popc(mb & below);
-        if (hb >> lane & 1u && hi < p.max_moves) to_list[hi] = i;
-        if (mb >> lane & 1u && mi < p.max_moves) from_list[mi] = i;
-        hole += __popc(hb);
-        mover += __popc(mb);
+        const bool is_hole = moves && i < p.keep;
+        const uint32_t both = __ballot_sync(0xFFFFFFFFu, moves);
+        if (!both) return;
+        const uint32_t h = __ballot_sync(0xFFFFFFFFu, is_hole), m = both ^ h;
+        const uint32_t at = is_hole ? hole + __popc(h & below) : mover + __popc(m & below);
+        if (moves && at < p.max_moves) (is_hole ? to_list : from_list)[at] = i;
+        hole += __popc(h);
+        mover += __popc(m);
     });
     if (blocks > 1) cluster_sync();  // no block leaves while another reads its counts
 }
@@ -485,18 +508,22 @@ cudaError_t launch_evict(const EvictParams& p, cudaStream_t s) {
     cudaError_t err = kernel_fit(reinterpret_cast<const void*>(evict_select_kernel<0>), kThreads, 0, &sms, &per_sm);
     if (err != cudaSuccess) return err;
     // As many blocks a list as fit on the device at once, while a thread has more
-    // than 4 keys (8 keys a thread take 12 us in one block, 16 take 25 and 32
-    // take 47; the cluster's barriers cost 4 us, more than fewer keys than that
-    // save), and at least as many as hold the longest sequence's keys, 32 a
-    // thread (beyond 8 blocks the keys are read again for every pass).
+    // than 8 keys (8,192 tokens, 8 heads: 9.8 us in one block, 12.3 in two, whose
+    // barriers cost more than the keys; 16,384: 25 us in one block with 16 of
+    // 32 keys, 13 in two or four), and at least as many as hold the longest
+    // sequence's keys, 32 a thread (beyond 8 blocks the keys are read again for
+    // every pass: 161 us for 524,288 tokens, 36 for 262,144).  16 keys have a
+    // kernel of their own: 32 spill, and 65,536 tokens in 32 lists take 23 us
+    // with it, 35 without.
     const uint64_t lists = (uint64_t)p.pool.heads * p.batch, longest = (uint64_t)p.table_width << p.pool.lg_page;
     uint32_t cluster = 1;
-    while (cluster < kMaxCluster && longest > 4ull * cluster * kThreads &&
+    while (cluster < kMaxCluster && longest > 8ull * cluster * kThreads &&
            (lists * cluster * 2 <= (uint64_t)sms || longest > 32ull * cluster * kThreads))
         cluster *= 2;
     const uint64_t keys = (longest + (uint64_t)cluster * kThreads - 1) / ((uint64_t)cluster * kThreads);
     err = launch_select(keys <= 2    ? evict_select_kernel<2>
                         : keys <= 8  ? evict_select_kernel<8>
+                        : keys <= 16 ? evict_select_kernel<16>
                         : keys <= 32 ? evict_select_kernel<32>
                                      : evict_select_kernel<0>,
                         p, cluster, s);

@@ -216,3 +216,19 @@ def test_many_lists(batch, heads, spread):
     got, st = run(pool, table, lens, weight, pos, next_pos, heads, dim, page, keep, recent)
     assert st == 0
     same(got, reference(pool, table, lens, weight, pos, next_pos, heads, dim, page, keep, recent))
+
+
+@pytest.mark.parametrize("n", [8192, 8193, 100000, 131073])
+@pytest.mark.parametrize("width", [8192, 16384, 131072, 262144, 1 << 20])
+def test_room_in_the_table(n, width):
+    """The table's width alone chooses how many keys a thread holds and how
+    many blocks share a list: few tokens in a wide table and a full one."""
+    heads, dim, page = 1, 64, 128
+    if n > width:
+        n = width
+    pool, table, lens, weight, pos = make([n, 3, n // 2], heads, dim, page, seed=n, width=width // page)
+    weight = (weight * 64).floor() / 64
+    keep, recent = n - 700, 300
+    got, st = run(pool, table, lens, weight, pos, lens, heads, dim, page, keep, recent)
+    assert st == 0
+    same(got, reference(pool, table, lens, weight, pos, lens, heads, dim, page, keep, recent))
