@@ -415,3 +415,31 @@ def test_items_of_their_own_blocks(tokens, heads, group):
     out, lse, st = run(pool, table, lens, q, heads, page, 0.125)
     assert st == 0
     check(out, lse, pool, table, lens, q, heads, page, 0.125)
+
+
+@pytest.mark.parametrize("test,args", [
+    (test_groups, (64, 7)), (test_groups, (128, 20)), (test_lengths_around_cells_units_and_pages, (16, True)),
+    (test_ranges, (30.0, 1.0, 0.3)), (test_ranges, (2.0 ** -60, 2.0 ** 58, 0.2)), (test_rising_logits, ()),
+    (test_slots_past_the_length_may_hold_anything, (True,)), (test_nan_stays_in_its_sequence_and_head, ()),
+    (test_bad_lengths_and_pages_are_reported, (True,)), (test_strided_and_unaligned_queries, ()),
+    (test_pages_shared_by_sequences, ()), (test_graph_with_other_lengths_and_another_stream, ()),
+    (test_non_finite_queries_stay_in_their_head, (math.inf,)), (test_unaligned_weights, ()),
+    (test_many_query_heads, (3, 33, 128))])
+def test_the_same_in_wide_tables(test, args, monkeypatch):
+    """Small cases again with room for 16,384 tokens in the table, where items
+    are dealt out to warps in runs and joined by the second kernel."""
+    plain_make, plain_run = make, run
+
+    def wide(table, page):
+        return torch.cat((table, torch.full((table.shape[0], 16384 // page - table.shape[1]), -1, dtype=torch.int32)), 1)
+
+    def wide_make(lens, heads, group, dim, page, *args, **kwargs):
+        pool, table, lens, q = plain_make(lens, heads, group, dim, page, *args, **kwargs)
+        return pool, wide(table, page), lens, q
+
+    def wide_run(pool, table, lens, q, heads, page, *args, **kwargs):
+        return plain_run(pool, wide(table, page), lens, q, heads, page, *args, **kwargs)
+
+    monkeypatch.setitem(globals(), "make", wide_make)
+    monkeypatch.setitem(globals(), "run", wide_run)
+    test(*args)
