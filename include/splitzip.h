@@ -466,8 +466,8 @@ size_t sz_cache_attend_workspace_size(size_t batch, size_t q_heads, size_t kv_he
  *  d_lens       int32 tokens per sequence.  An empty sequence gives zero rows
  *               (log-sum -infinity).  A length outside [0, table_width *
  *               page_tokens] counts as 0, the tokens of a page id outside the
- *               pool are left out; both are reported as SZ_ERR_INVALID_ARG in
- *               *d_status
+ *               pool are left out (a sequence with no others counts as empty);
+ *               both are reported as SZ_ERR_INVALID_ARG in *d_status
  *  d_lse        nullable: float [batch][q_heads], log of the sum of
  *               exp(scale * q k), for joining with another part of the context
  *  d_weight     nullable: each held slot's entry grows by the sum over its

@@ -39,6 +39,7 @@
 // 650 instructions per 32 tokens and warp; 12 warps per SM with 168 registers
 // are faster than 16 with 128 (62 against 64 us for 16 such sequences), and
 // the scales' and codes' unpacking keeps the integer pipe half busy.
+#include <cfloat>
 #include <type_traits>
 
 #include "sz_cache.cuh"
@@ -142,6 +143,9 @@ __device__ __forceinline__ uint32_t low_less8(uint32_t w) { return add_bf16x2(w 
 __device__ __forceinline__ uint32_t high_less8(uint32_t w) { return add_bf16x2(w & 0x00F000F0u, 0x80808080u); }
 // A reference to subtract from logits: 0 where there is no maximum yet.
 __device__ __forceinline__ float or_zero(float m) { return m == kNegInf ? 0.f : m; }
+// The factor that ends a row: 0 for a row without tokens (only those have the
+// maximum -infinity), whose sums are 0.
+__device__ __forceinline__ float inverse(float m, float l) { return m == kNegInf ? 0.f : 1.f / l; }
 
 // N (2 or 4) consecutive words of shared memory.
 template <int N>
@@ -422,6 +426,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attend_kernel(const
 
         float o[NT][2 * kG][4];
         float m[NT][2], l[NT][2];  // of heads 2t and 2t + 1; l: this thread's share of the sum of weights
+        uint32_t seen = 0;         // not 0 once there was a token
 #pragma unroll
         for (int n = 0; n < NT; n++) {
             m[n][0] = m[n][1] = kNegInf;
@@ -449,6 +454,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attend_kernel(const
             if (!alive) break;
             const uint8_t* u = ring + stage * Sh::kUnitBytes;
             const uint2 held = *reinterpret_cast<const uint2*>(counts + 2 * stage);  // tokens of the two cells
+            seen |= held.x | held.y;
             auto take_unit = [&](auto partial) {
                 constexpr bool PARTIAL = decltype(partial)::value;
                 // S: s[n][c][2 r + k] is token 16 c + 8 r + g, head 8 n + 2 t + k.
@@ -618,6 +624,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attend_kernel(const
                 l[n][k] += __shfl_xor_sync(0xFFFFFFFFu, l[n][k], 8);
                 l[n][k] += __shfl_xor_sync(0xFFFFFFFFu, l[n][k], 16);
                 l[n][k] *= 2.0194839173657902e-28f;
+                // Tokens whose logits are all -infinity are no empty row.
+                if (seen) m[n][k] = fmaxf(m[n][k], -FLT_MAX);
             }
 #pragma unroll
             for (int j = 0; j < 2 * kG; j++) {
@@ -626,7 +634,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attend_kernel(const
             }
             const uint32_t h = 8 * n + 2 * t;
             if (starts && ends) {
-                const float i0 = 1.f / l[n][0], i1 = 1.f / l[n][1];
+                const float i0 = inverse(m[n][0], l[n][0]), i1 = inverse(m[n][1], l[n][1]);
                 uint16_t* dst = p.out + (int64_t)seq * p.out_seq + (int64_t)(head0 + h) * p.out_head + 4 * g;
 #pragma unroll
                 for (int i = 0; i < kG; i++) {
@@ -712,7 +720,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attend_kernel(const
                 a[0] = fmaf(f, v.x, a[0]), a[1] = fmaf(f, v.y, a[1]), a[2] = fmaf(f, v.z, a[2]), a[3] = fmaf(f, v.w, a[3]);
             }
             if (w0 >= 0 && ends) {
-                const float inv = 1.f / l;
+                const float inv = inverse(top, l);
                 uint16_t* dst = p.out + (int64_t)seq * p.out_seq + (int64_t)(head0 + h) * p.out_head + c;
 #pragma unroll
                 for (int k = 0; k < 4; k++) dst[k] = (uint16_t)bf16_bits(a[k] * inv);
@@ -767,7 +775,7 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const AttendParams p, 
             l = fmaf(f, ml.y, l);
             a[0] = fmaf(f, v.x, a[0]), a[1] = fmaf(f, v.y, a[1]), a[2] = fmaf(f, v.z, a[2]), a[3] = fmaf(f, v.w, a[3]);
         }
-        const float inv = 1.f / l;
+        const float inv = inverse(top, l);
         uint16_t* dst = p.out + (int64_t)b * p.out_seq + (int64_t)(head0 + h) * p.out_head + c;
 #pragma unroll
         for (int k = 0; k < 4; k++) dst[k] = (uint16_t)bf16_bits(a[k] * inv);
