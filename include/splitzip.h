@@ -474,7 +474,8 @@ size_t sz_cache_attend_workspace_size(size_t batch, size_t q_heads, size_t kv_he
  *               query heads of the attention weight.  Additions to a page that
  *               two sequences share come in unspecified order
  *  d_status     nullable; SZ_OK, SZ_ERR_INVALID_ARG, or SZ_ERR_TIMEOUT when an
- *               in-kernel copy did not land within about 1 s
+ *               in-kernel copy did not land within about 1 s: the rows that
+ *               lack its tokens are NaN then, and d_weight is left as it was
  *  d_ws         256-byte aligned workspace, contents irrelevant
  * For the product with V a weight times its group's scale is rounded to
  * bfloat16.  Results do not depend on the timing of blocks.  Range: query
@@ -486,6 +487,16 @@ sz_status sz_cache_attend(const void* d_q, int64_t q_seq_stride, int64_t q_head_
                           const int32_t* d_table, size_t table_width, const int32_t* d_lens, float scale, void* d_out,
                           int64_t out_seq_stride, int64_t out_head_stride, float* d_lse, float* d_weight,
                           int* d_status, void* d_ws, size_t ws_bytes, cudaStream_t stream);
+
+/* Testing hook, not for production use: sz_cache_attend, except that the waits
+ * of its first block give up at once, as if their copies had not landed within
+ * the limit (they do land).  d_status must not be NULL. */
+sz_status sz_debug_attend_stalled(const void* d_q, int64_t q_seq_stride, int64_t q_head_stride, size_t batch,
+                                  size_t q_heads, const void* d_pool, size_t pool_pages, size_t kv_heads,
+                                  size_t head_dim, size_t page_tokens, const int32_t* d_table, size_t table_width,
+                                  const int32_t* d_lens, float scale, void* d_out, int64_t out_seq_stride,
+                                  int64_t out_head_stride, float* d_lse, float* d_weight, int* d_status, void* d_ws,
+                                  size_t ws_bytes, cudaStream_t stream);
 
 /* Bytes of device workspace for sz_cache_evict.  Host only; 0 for sizes
  * outside the limits. */

@@ -194,6 +194,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attend_kernel(const
     uint32_t* s_len = reinterpret_cast<uint32_t*>(smem + Sh::kLen);
     __shared__ uint32_t s_sum[W];
     __shared__ Left s_left[W];
+    __shared__ uint32_t s_gave_up;
     const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31u, g = lane >> 2, t = lane & 3u;
     const uint32_t items = p.pool.heads * p.tiles;
     const uint32_t lg_page = p.pool.lg_page;
@@ -206,6 +207,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attend_kernel(const
         for (int k = 0; k < Sh::kStages; k++) mbar_init(&bars[k], 1);
         fence_mbar_init();
         s_left[warp] = Left{0, 0, 0, 0, 0};
+        if (warp == 0) s_gave_up = 0;
     }
     wait_for_previous();
 
@@ -440,11 +442,15 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attend_kernel(const
 #pragma unroll 1
         for (uint32_t unit = r0; unit < r1; unit++) {
             if (alive) {
-                alive = __all_sync(0xFFFFFFFFu, mbar_wait(&bars[stage], phase, p.wait_limit_ns));
+                alive = __all_sync(0xFFFFFFFFu,
+                                   blockIdx.x != p.stalled_block && mbar_wait(&bars[stage], phase, p.wait_limit_ns));
                 if (!alive) {
                     // The copies still under way must land before the block
                     // gives its shared memory back.
-                    if (lane == 0 && p.status) atomicMax(p.status, kStatusTimeout);
+                    if (lane == 0) {
+                        s_gave_up = 1;
+                        if (p.status) atomicMax(p.status, kStatusTimeout);
+                    }
                     for (uint32_t k = 0, st = stage, ph = phase; k < in_flight; k++) {
                         mbar_wait(&bars[st], ph, p.wait_limit_ns);
                         if (++st == (uint32_t)Sh::kStages) st = 0, ph ^= 1u;
@@ -614,6 +620,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attend_kernel(const
         // Sums of weights are in units of 2^-92, code sums times 2^-41 (odd
         // channels 2^-37).
         const bool first_piece = !starts;
+        seen |= !alive;
         float* piece = reinterpret_cast<float*>(first_piece ? smem + Sh::kPiece + warp * Sh::kPieceBytes : ring);
         if (!starts || !ends) __syncwarp();
 #pragma unroll
@@ -623,7 +630,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attend_kernel(const
                 l[n][k] += __shfl_xor_sync(0xFFFFFFFFu, l[n][k], 4);
                 l[n][k] += __shfl_xor_sync(0xFFFFFFFFu, l[n][k], 8);
                 l[n][k] += __shfl_xor_sync(0xFFFFFFFFu, l[n][k], 16);
-                l[n][k] *= 2.0194839173657902e-28f;
+                // A row that lacks tokens for a wait that gave up is NaN.
+                l[n][k] = alive ? l[n][k] * 2.0194839173657902e-28f : __int_as_float(0x7FC00000);
                 // Tokens whose logits are all -infinity are no empty row.
                 if (seen) m[n][k] = fmaxf(m[n][k], -FLT_MAX);
             }
@@ -690,6 +698,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attend_kernel(const
 
     // ---- join the pieces of items that several warps of this block hold ----
     __syncthreads();
+    if (tid == 0) p.meta[4 * blockIdx.x + 3] = (int32_t)s_gave_up;
     auto first_of = [&](int w) { return reinterpret_cast<const float*>(smem + Sh::kPiece + w * Sh::kPieceBytes); };
     for (int w0 = -1; w0 < W; w0++) {
         // w0 = -1: the item that the block before this one left; else the one
@@ -791,8 +800,13 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const AttendParams p, 
 // weight[slot] += sum over the kv head's query heads of the step's attention
 // weight, from the logits that the first kernel kept.  A slot gets one
 // addition per call and sequence; atomic, for pages that two sequences share.
-__global__ void __launch_bounds__(256) attend_weight_kernel(const AttendParams p) {
+// Adds nothing where a block of the first kernel has given up: its logits are
+// missing, and the call can be made again with the weights as they were.
+__global__ void __launch_bounds__(256) attend_weight_kernel(const AttendParams p, const uint32_t first_blocks) {
     wait_for_previous();
+    int gave_up = 0;
+    for (uint32_t k = threadIdx.x; k < first_blocks; k += 256) gave_up |= p.meta[4 * k + 3];
+    if (__syncthreads_or(gave_up)) return;
     const uint32_t b = blockIdx.z, kv_head = blockIdx.y;
     const int32_t len = p.lens[b];
     const uint64_t max_tokens = (uint64_t)p.table_width << p.pool.lg_page;
@@ -848,13 +862,14 @@ cudaError_t launch(const AttendParams& p, cudaStream_t s) {
     const uint64_t unit_a_warp = (uint64_t)Sh::kWarps * kUnitTokens;
     AttendParams q = p;
     q.whole_items = items <= (uint64_t)sms && tokens <= (2 * items >= (uint64_t)sms ? 4 : 3) * unit_a_warp;
-    err = launch_dependent(attend_kernel<D, NT, LOGITS>, dim3(q.whole_items ? (uint32_t)items : (uint32_t)sms), dim3(Sh::kThreads),
-                           Sh::kBytes, s, q);
+    const uint32_t first_blocks = q.whole_items ? (uint32_t)items : (uint32_t)sms;
+    err = launch_dependent(attend_kernel<D, NT, LOGITS>, dim3(first_blocks), dim3(Sh::kThreads), Sh::kBytes, s, q);
     if (err != cudaSuccess) return err;
     if (!q.whole_items) err = launch_dependent(attend_join_kernel<D>, dim3((uint32_t)sms), dim3(256), 0, s, p, (uint32_t)Sh::kHeads);
     if (err != cudaSuccess || !LOGITS) return err;
     const uint32_t blocks = (uint32_t)((tokens + 1023) / 1024);
-    return launch_dependent(attend_weight_kernel, dim3(blocks < 1024 ? blocks : 1024, p.pool.heads, p.batch), dim3(256), 0, s, p);
+    return launch_dependent(attend_weight_kernel, dim3(blocks < 1024 ? blocks : 1024, p.pool.heads, p.batch), dim3(256), 0, s, p,
+                            first_blocks);
 }
 
 template <int D>

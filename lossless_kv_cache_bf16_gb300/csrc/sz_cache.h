@@ -68,10 +68,12 @@ struct AttendParams {
     float* weight;     // nullable
     int* status;       // nullable
     uint64_t wait_limit_ns;
+    uint32_t stalled_block;  // test hook: its waits give up at once, though their copies land
     int whole_items;  // one item a block (set by the launch)
     int q_vec, out_vec, weight_vec;  // query rows are 16-byte, output rows 8-byte, weights 16-byte aligned
     // workspace
-    int32_t* meta;   // [blocks][4]
+    int32_t* meta;   // [blocks][4]: the item that a block leaves to the join (sequence or -1, item, further blocks),
+                     // whether a wait of the block gave up
     float* part_ml;  // [blocks][2][16][2]: maximum, sum of weights
     float* part_o;   // [blocks][2][16][dim]
     float* lse2;     // [batch][q heads], log2; with weight

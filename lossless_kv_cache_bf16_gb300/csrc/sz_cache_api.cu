@@ -14,6 +14,7 @@ namespace {
 using namespace sz;
 
 constexpr uint64_t kWaitLimitNs = 1000000000ull;  // bounded in-kernel waits for asynchronous copies: 1 s
+constexpr uint32_t kNoBlock = 0xFFFFFFFFu;
 
 struct NvtxRange {
     explicit NvtxRange(const char* name) { nvtxRangePushA(name); }
@@ -106,6 +107,59 @@ bool attend_sizes_ok(size_t batch, size_t q_heads, size_t kv_heads, size_t dim, 
 
 uint64_t evict_max_moves(uint64_t max_tokens) { return (max_tokens + 1) / 2; }
 uint64_t evict_pairs_offset(uint64_t lists) { return align256(4 * lists); }
+
+sz_status attend(const char* name, uint32_t stalled_block, const void* d_q, int64_t q_seq_stride, int64_t q_head_stride,
+                 size_t batch, size_t q_heads, const void* d_pool, size_t pool_pages, size_t kv_heads, size_t head_dim,
+                 size_t page_tokens, const int32_t* d_table, size_t table_width, const int32_t* d_lens, float scale,
+                 void* d_out, int64_t out_seq_stride, int64_t out_head_stride, float* d_lse, float* d_weight, int* d_status,
+                 void* d_ws, size_t ws_bytes, cudaStream_t stream) {
+    const NvtxRange range(name);
+    AttendParams p{};
+    if (!pool_for(d_pool, pool_pages, kv_heads, head_dim, page_tokens, &p.pool)) return SZ_ERR_INVALID_ARG;
+    if (batch > 0 && !table_ok(d_table, table_width, page_tokens)) return SZ_ERR_INVALID_ARG;
+    const uint64_t max_tokens = batch > 0 ? (uint64_t)table_width * page_tokens : page_tokens;
+    if (!attend_sizes_ok(batch, q_heads, kv_heads, head_dim, max_tokens) || !std::isfinite(scale)) return SZ_ERR_INVALID_ARG;
+    if ((d_status && !aligned(d_status, 4)) || (d_lse && !aligned(d_lse, 4)) || (d_weight && !aligned(d_weight, 4)))
+        return SZ_ERR_INVALID_ARG;
+    if (batch > 0 && (!d_q || !d_out || !aligned(d_q, 2) || !aligned(d_out, 2) || !d_lens || !aligned(d_lens, 4) || !d_ws ||
+                      !aligned(d_ws, 256)))
+        return SZ_ERR_INVALID_ARG;
+    if (batch == 0) return clear_status(d_status, stream);
+    uint32_t item_heads = 0, blocks = 0;
+    const uint32_t group = (uint32_t)(q_heads / kv_heads);
+    const cudaError_t err = attend_shape(group, &item_heads, &blocks);
+    if (err != cudaSuccess) return from_cuda(err);
+    const AttendWs w = attend_ws(blocks, head_dim, batch * q_heads, max_tokens, d_weight != nullptr);
+    if (ws_bytes < w.end) return SZ_ERR_CAPACITY;
+    const sz_status st = clear_status(d_status, stream);
+    if (st != SZ_OK) return st;
+    uint8_t* ws = static_cast<uint8_t*>(d_ws);
+    p.q = static_cast<const uint16_t*>(d_q);
+    p.q_seq = q_seq_stride, p.q_head = q_head_stride;
+    p.out = static_cast<uint16_t*>(d_out);
+    p.out_seq = out_seq_stride, p.out_head = out_head_stride;
+    p.table = d_table;
+    p.table_width = (uint32_t)table_width;
+    p.lens = d_lens;
+    p.batch = (uint32_t)batch;
+    p.group = group;
+    p.tiles = (group + item_heads - 1) / item_heads;
+    p.scale_log2 = (float)((double)scale * 1.4426950408889634);
+    p.lse = d_lse;
+    p.weight = d_weight;
+    p.status = d_status;
+    p.wait_limit_ns = kWaitLimitNs;
+    p.stalled_block = stalled_block;
+    p.q_vec = aligned(d_q, 16) && multiple(q_seq_stride, q_head_stride, 8);
+    p.weight_vec = aligned(d_weight, 16);
+    p.out_vec = aligned(d_out, 8) && multiple(out_seq_stride, out_head_stride, 4);
+    p.meta = reinterpret_cast<int32_t*>(ws);
+    p.part_ml = reinterpret_cast<float*>(ws + w.ml);
+    p.part_o = reinterpret_cast<float*>(ws + w.o);
+    p.lse2 = reinterpret_cast<float*>(ws + w.lse2);
+    p.logits = reinterpret_cast<float*>(ws + w.logits);
+    return from_cuda(launch_attend(p, stream));
+}
 
 }  // namespace
 
@@ -209,51 +263,20 @@ sz_status sz_cache_attend(const void* d_q, int64_t q_seq_stride, int64_t q_head_
                           const int32_t* d_table, size_t table_width, const int32_t* d_lens, float scale, void* d_out,
                           int64_t out_seq_stride, int64_t out_head_stride, float* d_lse, float* d_weight,
                           int* d_status, void* d_ws, size_t ws_bytes, cudaStream_t stream) {
-    const NvtxRange range("sz_cache_attend");
-    AttendParams p{};
-    if (!pool_for(d_pool, pool_pages, kv_heads, head_dim, page_tokens, &p.pool)) return SZ_ERR_INVALID_ARG;
-    if (batch > 0 && !table_ok(d_table, table_width, page_tokens)) return SZ_ERR_INVALID_ARG;
-    const uint64_t max_tokens = batch > 0 ? (uint64_t)table_width * page_tokens : page_tokens;
-    if (!attend_sizes_ok(batch, q_heads, kv_heads, head_dim, max_tokens) || !std::isfinite(scale)) return SZ_ERR_INVALID_ARG;
-    if ((d_status && !aligned(d_status, 4)) || (d_lse && !aligned(d_lse, 4)) || (d_weight && !aligned(d_weight, 4)))
-        return SZ_ERR_INVALID_ARG;
-    if (batch > 0 && (!d_q || !d_out || !aligned(d_q, 2) || !aligned(d_out, 2) || !d_lens || !aligned(d_lens, 4) || !d_ws ||
-                      !aligned(d_ws, 256)))
-        return SZ_ERR_INVALID_ARG;
-    if (batch == 0) return clear_status(d_status, stream);
-    uint32_t item_heads = 0, blocks = 0;
-    const uint32_t group = (uint32_t)(q_heads / kv_heads);
-    const cudaError_t err = attend_shape(group, &item_heads, &blocks);
-    if (err != cudaSuccess) return from_cuda(err);
-    const AttendWs w = attend_ws(blocks, head_dim, batch * q_heads, max_tokens, d_weight != nullptr);
-    if (ws_bytes < w.end) return SZ_ERR_CAPACITY;
-    const sz_status st = clear_status(d_status, stream);
-    if (st != SZ_OK) return st;
-    uint8_t* ws = static_cast<uint8_t*>(d_ws);
-    p.q = static_cast<const uint16_t*>(d_q);
-    p.q_seq = q_seq_stride, p.q_head = q_head_stride;
-    p.out = static_cast<uint16_t*>(d_out);
-    p.out_seq = out_seq_stride, p.out_head = out_head_stride;
-    p.table = d_table;
-    p.table_width = (uint32_t)table_width;
-    p.lens = d_lens;
-    p.batch = (uint32_t)batch;
-    p.group = group;
-    p.tiles = (group + item_heads - 1) / item_heads;
-    p.scale_log2 = (float)((double)scale * 1.4426950408889634);
-    p.lse = d_lse;
-    p.weight = d_weight;
-    p.status = d_status;
-    p.wait_limit_ns = kWaitLimitNs;
-    p.q_vec = aligned(d_q, 16) && multiple(q_seq_stride, q_head_stride, 8);
-    p.weight_vec = aligned(d_weight, 16);
-    p.out_vec = aligned(d_out, 8) && multiple(out_seq_stride, out_head_stride, 4);
-    p.meta = reinterpret_cast<int32_t*>(ws);
-    p.part_ml = reinterpret_cast<float*>(ws + w.ml);
-    p.part_o = reinterpret_cast<float*>(ws + w.o);
-    p.lse2 = reinterpret_cast<float*>(ws + w.lse2);
-    p.logits = reinterpret_cast<float*>(ws + w.logits);
-    return from_cuda(launch_attend(p, stream));
+    return attend("sz_cache_attend", kNoBlock, d_q, q_seq_stride, q_head_stride, batch, q_heads, d_pool, pool_pages, kv_heads,
+                  head_dim, page_tokens, d_table, table_width, d_lens, scale, d_out, out_seq_stride, out_head_stride, d_lse,
+                  d_weight, d_status, d_ws, ws_bytes, stream);
+}
+
+sz_status sz_debug_attend_stalled(const void* d_q, int64_t q_seq_stride, int64_t q_head_stride, size_t batch, size_t q_heads,
+                                  const void* d_pool, size_t pool_pages, size_t kv_heads, size_t head_dim,
+                                  size_t page_tokens, const int32_t* d_table, size_t table_width, const int32_t* d_lens,
+                                  float scale, void* d_out, int64_t out_seq_stride, int64_t out_head_stride, float* d_lse,
+                                  float* d_weight, int* d_status, void* d_ws, size_t ws_bytes, cudaStream_t stream) {
+    if (!d_status) return SZ_ERR_INVALID_ARG;
+    return attend("sz_debug_attend_stalled", 0, d_q, q_seq_stride, q_head_stride, batch, q_heads, d_pool, pool_pages, kv_heads,
+                  head_dim, page_tokens, d_table, table_width, d_lens, scale, d_out, out_seq_stride, out_head_stride, d_lse,
+                  d_weight, d_status, d_ws, ws_bytes, stream);
 }
 
 size_t sz_cache_evict_workspace_size(size_t batch, size_t kv_heads, size_t max_tokens) {

@@ -85,6 +85,8 @@ def _load() -> ctypes.CDLL:
         "sz_cache_attend_workspace_size": (sz, [sz, sz, sz, sz, sz, i32]),
         "sz_cache_attend": (i32, [vp, i64, i64, sz, sz, vp, sz, sz, sz, sz, vp, sz, vp, ctypes.c_float, vp, i64, i64,
                                   vp, vp, vp, vp, sz, vp]),
+        "sz_debug_attend_stalled": (i32, [vp, i64, i64, sz, sz, vp, sz, sz, sz, sz, vp, sz, vp, ctypes.c_float, vp, i64,
+                                          i64, vp, vp, vp, vp, sz, vp]),
         "sz_cache_evict_workspace_size": (sz, [sz, sz, sz]),
         "sz_cache_evict": (i32, [vp, sz, sz, sz, sz, vp, sz, vp, vp, sz, sz, sz, vp, vp, vp, vp, vp, sz, vp]),
     }
@@ -100,7 +102,8 @@ LIB = _load()
 from . import _sz_bind as _bind  # noqa: E402  (built with the library)
 
 _ADDRESS = {name: ctypes.cast(getattr(LIB, name), ctypes.c_void_p).value
-            for name in ("sz_qk_norm_rope", "sz_cache_append", "sz_cache_read", "sz_cache_attend", "sz_cache_evict")}
+            for name in ("sz_qk_norm_rope", "sz_cache_append", "sz_cache_read", "sz_cache_attend", "sz_debug_attend_stalled",
+                         "sz_cache_evict")}
 
 
 # ---- marshalling helpers -----------------------------------------------------
@@ -518,6 +521,16 @@ def sz_cache_attend(q: torch.Tensor, pool: torch.Tensor, kv_heads: int, page_tok
     cache: sequence b's lens[b] tokens lie in the pages table[b].  lse (fp32
     [batch, q heads]) gets the log-sums; weight (fp32, one entry per page, kv
     head and offset) grows by the attention weights."""
+    _attend("sz_cache_attend", q, pool, kv_heads, page_tokens, table, lens, scale, out, ws, lse, weight, status, stream)
+
+
+def sz_debug_attend_stalled(q, pool, kv_heads: int, page_tokens: int, table, lens, scale: float, out, ws, lse=None,
+                            weight=None, status=None, stream=None) -> None:
+    """sz_cache_attend with waits that give up (a testing hook)."""
+    _attend("sz_debug_attend_stalled", q, pool, kv_heads, page_tokens, table, lens, scale, out, ws, lse, weight, status, stream)
+
+
+def _attend(name, q, pool, kv_heads, page_tokens, table, lens, scale, out, ws, lse, weight, status, stream) -> None:
     qp, shape, qs = _rows(q, _BF16, "q")
     batch, q_heads, d = shape
     op, _, os = _written_rows(out, _BF16, shape, "out")
@@ -525,8 +538,8 @@ def sz_cache_attend(q: torch.Tensor, pool: torch.Tensor, kv_heads: int, page_tok
         raise ValueError("out must not be q")
     pages = _cache_pages(pool, kv_heads, d, page_tokens)
     table_ptr, width = _table(table, batch)
-    _check("sz_cache_attend", _bind.cache_attend(
-        _ADDRESS["sz_cache_attend"], qp, qs[0], qs[1], batch, q_heads, _pointer(pool, None, -1, "pool"), pages, kv_heads,
+    _check(name, _bind.cache_attend(
+        _ADDRESS[name], qp, qs[0], qs[1], batch, q_heads, _pointer(pool, None, -1, "pool"), pages, kv_heads,
         d, page_tokens, table_ptr, width, _pointer(lens, _I32, batch, "lens"), scale, op, os[0], os[1],
         _pointer(lse, _F32, batch * q_heads, "lse"), _pointer(weight, _F32, pages * kv_heads * page_tokens, "weight"),
         _pointer(status, _I32, 1, "status"), _pointer(ws, None, -1, "ws"), ws.numel() * ws.element_size(),

@@ -1,4 +1,5 @@
-"""Attention over the 4-bit cache: rows that no token reaches.
+"""Attention over the 4-bit cache: rows that no token reaches, waits that give
+up.
 
 Tolerances are those of tests/test_gpu_attend.py.
 """
@@ -57,3 +58,39 @@ def test_logits_past_the_range_are_no_empty_row(n, room):
     table = widen(torch.arange(pages, dtype=torch.int32)[None], page, room)
     out, lse, st = run(pool, table, torch.tensor([n], dtype=torch.int32), q, heads, page, 1.0)
     assert st == 0 and not bool(torch.isfinite(out).any())
+
+
+@pytest.mark.parametrize("room", [None, 16384])
+@pytest.mark.parametrize("weighted", [False, True])
+@pytest.mark.parametrize("dim,heads,group,sizes", [
+    (128, 2, 4, [300, 40, 33, 0, 500]), (64, 1, 12, [700, 1]), (128, 1, 8, [6000]), (64, 4, 2, [30] * 200)])
+def test_a_wait_that_gives_up_leaves_the_weights_alone(dim, heads, group, sizes, weighted, room):
+    """The first block's waits give up: its rows are NaN, the others right, the
+    status says so, and the accumulated weights can be used for another try."""
+    from lossless_kv_cache_bf16_gb300 import splitzip as S
+
+    page = 16
+    pool, table, lens, q = make(sizes, heads, group, dim, page, seed=50 + group)
+    table = widen(table, page, room)
+    b, hq = len(sizes), heads * group
+    weight0 = torch.rand(pool.shape[0], heads, page, generator=R.gen(1))
+    want, want_lse, st = run(pool, table, lens, q, heads, page, 0.1, weight=weight0.cuda() if weighted else None)
+    assert st == 0
+    need = S.sz_cache_attend_workspace_size(b, hq, heads, dim, table.shape[1] * page, weighted)
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")
+    out, lse = torch.zeros(q.shape, dtype=torch.bfloat16, device="cuda"), torch.zeros(b, hq, device="cuda")
+    weight = weight0.cuda() if weighted else None
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    args = (q.cuda(), pool.cuda(), heads, page, table.cuda(), lens.cuda(), 0.1, out, ws)
+    for _ in range(2):
+        S.sz_debug_attend_stalled(*args, lse=lse, weight=weight, status=status)
+        assert int(status) == S.SZ_ERR_TIMEOUT
+        lost = torch.isnan(lse)
+        assert bool(lost[0, 0]) and (len(sizes) == 1 or not bool(lost.all()))
+        assert bool(torch.isnan(out[lost]).all())
+        assert torch.equal(out[~lost], want[~lost]) and torch.equal(lse[~lost], want_lse[~lost])
+        if weighted:
+            assert torch.equal(weight.cpu(), weight0)
+    S.sz_cache_attend(*args, lse=lse, weight=weight, status=status)
+    assert int(status) == 0 and torch.equal(out, want) and torch.equal(lse, want_lse)
+    check(out, lse, pool, table, lens, q, heads, page, 0.1, weight0, weight)
