@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attend_kernel(const
     constexpr int W = Sh::kWarps, kG = C::kGroups, kSteps = D / 16;
     extern __shared__ __align__(128) uint8_t smem[];
     uint32_t* s_len = reinterpret_cast<uint32_t*>(smem + Sh::kLen);
-    __shared__ uint32_t s_sum[W];
+    __shared__ uint64_t s_sum[W];
     __shared__ Left s_left[W];
     __shared__ uint32_t s_gave_up;
     const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31u, g = lane >> 2, t = lane & 3u;
@@ -221,8 +221,11 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attend_kernel(const
         s_len[b] = ok ? (uint32_t)len : 0u;
         mine += ok ? entries((uint32_t)len) : 0u;
     }
-    mine = __reduce_add_sync(0xFFFFFFFFu, mine);
-    if (lane == 0) s_sum[warp] = mine;
+    // A thread's sum stays below 2^30 (at most 8 sequences of 2^26 units), a
+    // warp's need not stay below 2^32: its halves are added up apart.
+    const uint64_t of_warp = __reduce_add_sync(0xFFFFFFFFu, mine & 0xFFFFu) +
+                             ((uint64_t)__reduce_add_sync(0xFFFFFFFFu, mine >> 16) << 16);
+    if (lane == 0) s_sum[warp] = of_warp;
     __syncthreads();
     uint64_t total = 0;
     for (int w = 0; w < W; w++) total += s_sum[w];

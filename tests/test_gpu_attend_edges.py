@@ -94,3 +94,34 @@ def test_a_wait_that_gives_up_leaves_the_weights_alone(dim, heads, group, sizes,
     S.sz_cache_attend(*args, lse=lse, weight=weight, status=status)
     assert int(status) == 0 and torch.equal(out, want) and torch.equal(lse, want_lse)
     check(out, lse, pool, table, lens, q, heads, page, 0.1, weight0, weight)
+
+
+def test_more_list_entries_than_32_bits():
+    """65 sequences of 2^26 units each, all of one page, whose lengths one warp
+    adds up: 2^32 entries and more.  The short sequence behind them is the last
+    of the list."""
+    from lossless_kv_cache_bf16_gb300 import splitzip as S
+
+    heads, group, dim, page, width = 1, 1, 64, 4096, 2 ** 19 - 1
+    longest = width * page
+    # A thread takes every 384th sequence, a warp 32 threads.
+    full = list(range(32)) + list(range(384, 416)) + [768]
+    batch, last = 770, 769
+    assert len(full) * (longest // 32) >= 2 ** 32
+    pool = R.fill(R.gen(60), 2, heads, page, dim)
+    table = torch.zeros((batch, width), dtype=torch.int32, device="cuda")
+    table[last] = 1
+    lens = torch.zeros(batch, dtype=torch.int32)
+    lens[full] = longest
+    lens[last] = 77
+    q = R.normal_bf16(R.gen(61), batch, heads * group, dim)
+    ws = torch.empty(S.sz_cache_attend_workspace_size(batch, group, heads, dim, longest), dtype=torch.uint8, device="cuda")
+    out = torch.full_like(q.cuda(), math.nan)
+    lse = torch.full((batch, group), math.nan, device="cuda")
+    st = torch.full((1,), -1, dtype=torch.int32, device="cuda")
+    S.sz_cache_attend(q.cuda(), pool.cuda(), heads, page, table, lens.cuda(), 0.1, out, ws, lse=lse, status=st)
+    assert int(st) == 0
+    assert bool(torch.isfinite(out).all()) and bool(torch.isfinite(lse[full]).all())
+    empty = lens == 0
+    assert bool((out[empty.cuda()] == 0).all()) and bool((lse[empty.cuda()] == -math.inf).all())
+    check(out[last:], lse[last:], pool, torch.ones(1, 1, dtype=torch.int32), lens[last:], q[last:], heads, page, 0.1)
