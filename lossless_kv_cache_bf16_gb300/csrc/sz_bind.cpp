@@ -3,7 +3,7 @@
 // the C ABI.  Interpreted, they cost more time than a decode step's kernels.
 //
 // It sees tensors only through their Python attributes (dtype, shape,
-// stride(), is_cuda, is_contiguous(), data_ptr()), and the library only
+// stride(), is_cuda, get_device(), is_contiguous(), data_ptr()), and the library only
 // through the addresses that splitzip.py passes, so that it depends on neither
 // PyTorch's headers nor the order in which libraries are loaded.
 #define PY_SSIZE_T_CLEAN
@@ -16,7 +16,7 @@
 
 namespace {
 
-PyObject *s_dtype, *s_shape, *s_stride, *s_is_cuda, *s_is_contiguous, *s_data_ptr, *s_numel;
+PyObject *s_dtype, *s_shape, *s_stride, *s_is_cuda, *s_is_contiguous, *s_data_ptr, *s_numel, *s_get_device;
 
 // An owned reference.
 struct Ref {
@@ -41,23 +41,47 @@ PyObject* refuse(PyObject* what, const char* why) {
     return nullptr;
 }
 
-bool expect(Py_ssize_t got, Py_ssize_t want) {
-    if (got == want) return true;
+// extra: how many further arguments may follow
+bool expect(Py_ssize_t got, Py_ssize_t want, Py_ssize_t extra = 0) {
+    if (got >= want && got <= want + extra) return true;
     PyErr_Format(PyExc_TypeError, "%zd arguments expected, not %zd", want, got);
     return false;
 }
 
+// Whether t is on the GPU of that number (on any one if it is negative): the
+// kernels run on the call's GPU, and a pointer into another would be followed
+// there.  False with an error.
+bool on_gpu(PyObject* t, long device, PyObject* what) {
+    if (device >= 0) {
+        Ref index(PyObject_CallMethodNoArgs(t, s_get_device));
+        if (!index) return false;
+        const long got = PyLong_AsLong(index.o);
+        if (got == device) return true;
+        if (got == -1 && PyErr_Occurred()) return false;
+    }
+    const int cuda = truth(PyObject_GetAttr(t, s_is_cuda));
+    if (cuda < 0) return false;
+    if (!cuda) return refuse(what, "must be a CUDA tensor");
+    if (device >= 0) return refuse(what, "must be on the GPU that the call runs on");
+    return true;
+}
+// The device argument after the first n, -1 without one; -2 with an error.
+long device_of(PyObject* const* a, Py_ssize_t n, Py_ssize_t got) {
+    if (got <= n) return -1;
+    const long d = PyLong_AsLong(a[n]);
+    return d == -1 && PyErr_Occurred() ? -2 : d;
+}
+
 // (data_ptr, shape, stride) of a bf16 CUDA tensor [rows, heads, channels] whose
 // channels are contiguous.
-PyObject* rows_of(PyObject* t, PyObject* bfloat16, PyObject* what) {
+PyObject* rows_of(PyObject* t, PyObject* bfloat16, PyObject* what, long device) {
+    if (device < -1) return nullptr;
     Ref dtype(PyObject_GetAttr(t, s_dtype)), shape(PyObject_GetAttr(t, s_shape)), stride(PyObject_CallMethodNoArgs(t, s_stride));
     if (!dtype || !shape || !stride) return nullptr;
     if (dtype.o != bfloat16 || !PyTuple_Check(shape.o) || !PyTuple_Check(stride.o) || PyTuple_GET_SIZE(shape.o) != 3 ||
         PyTuple_GET_SIZE(stride.o) != 3)
         return refuse(what, "must be a bfloat16 tensor of three dimensions");
-    const int cuda = truth(PyObject_GetAttr(t, s_is_cuda));
-    if (cuda < 0) return nullptr;
-    if (!cuda) return refuse(what, "must be a CUDA tensor");
+    if (!on_gpu(t, device, what)) return nullptr;
     const long long last = PyLong_AsLongLong(PyTuple_GET_ITEM(stride.o, 2));
     if (last != 1) {
         if (PyErr_Occurred()) return nullptr;
@@ -71,17 +95,20 @@ PyObject* rows_of(PyObject* t, PyObject* bfloat16, PyObject* what) {
     return PyTuple_Pack(3, ptr.o, shape.o, stride.o);
 }
 
-// rows(t, bfloat16, what)
+// The checks below take the number of the GPU that the call runs on as a last
+// argument; without it (or with -1) any will do.
+
+// rows(t, bfloat16, what[, device])
 PyObject* rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    return expect(n, 3) ? rows_of(a[0], a[1], a[2]) : nullptr;
+    return expect(n, 3, 1) ? rows_of(a[0], a[1], a[2], device_of(a, 3, n)) : nullptr;
 }
 
-// written_rows(t, bfloat16, shape, what): the same for a tensor of that shape
+// written_rows(t, bfloat16, shape, what[, device]): the same for a tensor of that shape
 // which a kernel writes: no two of its rows may share memory.
 PyObject* written_rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    if (!expect(n, 4)) return nullptr;
+    if (!expect(n, 4, 1)) return nullptr;
     PyObject* what = a[3];
-    Ref got(rows_of(a[0], a[1], what));
+    Ref got(rows_of(a[0], a[1], what, device_of(a, 4, n)));
     if (!got) return nullptr;
     PyObject *shape = PyTuple_GET_ITEM(got.o, 1), *stride = PyTuple_GET_ITEM(got.o, 2);
     const int same = PyObject_RichCompareBool(shape, a[2], Py_EQ);
@@ -112,12 +139,14 @@ PyObject* written_rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return got.o;
 }
 
-// pointer(t, dtype or None, count or -1, what) -> data_ptr of a contiguous CUDA
+// pointer(t, dtype or None, count or -1, what[, device]) -> data_ptr of a contiguous CUDA
 // tensor of that type with that many values; None for None.
 PyObject* pointer(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    if (!expect(n, 4)) return nullptr;
+    if (!expect(n, 4, 1)) return nullptr;
     PyObject *t = a[0], *what = a[3];
     if (t == Py_None) Py_RETURN_NONE;
+    const long device = device_of(a, 4, n);
+    if (device < -1) return nullptr;
     if (a[1] != Py_None) {
         Ref dtype(PyObject_GetAttr(t, s_dtype));
         if (!dtype) return nullptr;
@@ -138,9 +167,7 @@ PyObject* pointer(PyObject*, PyObject* const* a, Py_ssize_t n) {
             return nullptr;
         }
     }
-    const int cuda = truth(PyObject_GetAttr(t, s_is_cuda));
-    if (cuda < 0) return nullptr;
-    if (!cuda) return refuse(what, "must be a CUDA tensor");
+    if (!on_gpu(t, device, what)) return nullptr;
     const int dense = truth(PyObject_CallMethodNoArgs(t, s_is_contiguous));
     if (dense < 0) return nullptr;
     if (!dense) return refuse(what, "must be contiguous");
@@ -232,7 +259,8 @@ PyMODINIT_FUNC PyInit__sz_bind(void) {
         PyObject** at;
         const char* name;
     } names[] = {{&s_dtype, "dtype"}, {&s_shape, "shape"}, {&s_stride, "stride"}, {&s_is_cuda, "is_cuda"},
-                 {&s_is_contiguous, "is_contiguous"}, {&s_data_ptr, "data_ptr"}, {&s_numel, "numel"}};
+                 {&s_is_contiguous, "is_contiguous"}, {&s_data_ptr, "data_ptr"}, {&s_numel, "numel"},
+                 {&s_get_device, "get_device"}};
     for (auto& x : names)
         if (!(*x.at = PyUnicode_InternFromString(x.name))) return nullptr;
     return PyModule_Create(&module);

@@ -15,11 +15,24 @@ eviction change in the attention's result.
 """
 from __future__ import annotations
 
+import contextlib
+import functools
 import math
 
 import torch
 
 from . import splitzip as S
+
+
+def _on_its_gpu(method):
+    """Runs a DecodeCache method with the cache's GPU as the current one, whose
+    current stream the library's calls and torch's kernels then share."""
+    @functools.wraps(method)
+    def call(self, *args, **kwargs):
+        with self._gpu():
+            return method(self, *args, **kwargs)
+
+    return call
 
 
 class DecodeCache:
@@ -48,26 +61,36 @@ class DecodeCache:
         self.status = new(1, torch.int32)
         self.held = [0] * batch                       # the lengths, as the host knows them
         self.capacity = width * page_tokens
-        self.attend_ws = new(S.sz_cache_attend_workspace_size(batch, q_heads, kv_heads, head_dim, self.capacity, True), torch.uint8)
+        self.device = self.pool.device
+        with self._gpu():
+            need = S.sz_cache_attend_workspace_size(batch, q_heads, kv_heads, head_dim, self.capacity, True)
+        self.attend_ws = new(need, torch.uint8)
         self.evict_ws = new(S.sz_cache_evict_workspace_size(batch, kv_heads, self.capacity), torch.uint8)
 
+    def _gpu(self):
+        return torch.cuda.device(self.device) if self.device.type == "cuda" else contextlib.nullcontext()
+
+    @_on_its_gpu
     def extend(self, sequence: int, k: torch.Tensor, v: torch.Tensor) -> None:
         """Appends a prompt's rows [tokens, kv heads, D], keys already rotated."""
         n, at = k.shape[0], self.held[sequence]
         if at + n > self.capacity:
             raise ValueError(f"{at + n} tokens do not fit in {self.capacity}")
-        slot = torch.arange(at, at + n, device=k.device)
+        slot = torch.arange(at, at + n, device=self.device)
         slots = self.table[sequence].long()[slot // self.page] * self.page + slot % self.page
-        positions = self.next_pos[sequence] + torch.arange(n, dtype=torch.int32, device=k.device)
+        positions = self.next_pos[sequence] + torch.arange(n, dtype=torch.int32, device=self.device)
         S.sz_cache_append(k, v, slots, self.pool, self.page, positions=positions, weight=self.weight, pos=self.pos)
         self.lens[sequence] += n
         self.next_pos[sequence] += n
         self.held[sequence] += n
 
+    @_on_its_gpu
     def extend_from_stream(self, sequence: int, stream: torch.Tensor, nbytes: int, tokens: int) -> None:
         """Appends a prompt that arrives as the SplitZip stream of a bf16
         tensor [2 (K, V), tokens, kv heads, D]."""
-        kv = torch.empty((2, tokens, self.kv_heads, self.head_dim), dtype=torch.bfloat16, device=self.pool.device)
+        if stream.device != self.device:
+            raise ValueError(f"the stream must be on the cache's GPU ({self.device}), not on {stream.device}")
+        kv = torch.empty((2, tokens, self.kv_heads, self.head_dim), dtype=torch.bfloat16, device=self.device)
         S.sz_decode(S.SZ_BF16, stream, nbytes, kv.numel(), kv, self.status)
         self.check()
         self.extend(sequence, kv[0], kv[1])
@@ -78,6 +101,7 @@ class DecodeCache:
         if status != S.SZ_OK:
             raise S.SplitZipError("DecodeCache", status)
 
+    @_on_its_gpu
     def step(self, qkv: torch.Tensor, q_weight, k_weight, inv_freq: torch.Tensor, eps: float = 1e-6,
              out: torch.Tensor | None = None) -> torch.Tensor:
         """One token of every sequence: qkv [batch, q heads + 2 kv heads, D] as
@@ -94,13 +118,14 @@ class DecodeCache:
         self.next_pos += 1
         self.held = [n + 1 for n in self.held]
         if out is None:
-            out = torch.empty((self.batch, hq, self.head_dim), dtype=torch.bfloat16, device=qkv.device)
+            out = torch.empty((self.batch, hq, self.head_dim), dtype=torch.bfloat16, device=self.device)
         S.sz_cache_attend(q, self.pool, hk, self.page, self.table, self.lens, 1 / math.sqrt(self.head_dim), out,
                           self.attend_ws, weight=self.weight, status=self.status)
         if self.budget is not None and max(self.held) >= self.budget + self.page:
             self.evict()
         return out
 
+    @_on_its_gpu
     def evict(self) -> None:
         """Cuts every sequence longer than the budget to it."""
         S.sz_cache_evict(self.pool, self.kv_heads, self.head_dim, self.page, self.table, self.lens, self.next_pos,

@@ -3,7 +3,8 @@
 Argument marshalling only: every function forwards to ``libsplitzip.so`` with
 the same name, passing device pointers of torch CUDA tensors and the current
 CUDA stream (through ctypes; the serving operators, which are called once a
-layer and token, through the C++ module ``_sz_bind``).  All work runs in the library's CUDA kernels; there is no CPU
+layer and token, through the C++ module ``_sz_bind``, which refuses tensors of
+another GPU than the call's).  All work runs in the library's CUDA kernels; there is no CPU
 path, and importing this module fails loudly when the library is missing.
 """
 from __future__ import annotations
@@ -426,6 +427,22 @@ def sz_debug_encode_stalled(dt: int, cb, x: torch.Tensor, out: torch.Tensor, out
 _BF16, _F32, _I32, _I64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
 _rows, _written_rows, _pointer = _bind.rows, _bind.written_rows, _bind.pointer
 
+
+def _launch_on(stream):
+    """(GPU that the call's kernels run on, stream handle): all of its tensors
+    must be on that GPU.  -1, any, for an object that only has a handle."""
+    if stream is None:
+        if _raw_stream is None or _get_device is None:
+            stream = torch.cuda.current_stream()
+            return stream.device_index, stream.cuda_stream
+        device = _get_device()
+        return device, _raw_stream(device)
+    device = getattr(stream, "device_index", -1)
+    if device >= 0 and device != torch.cuda.current_device():
+        raise ValueError("stream must belong to the current GPU")
+    return device, stream.cuda_stream
+
+
 _PAGE_BYTES: dict = {}  # (head_dim, kv_heads, page_tokens) -> bytes of a page
 
 
@@ -441,11 +458,11 @@ def _cache_pages(pool: torch.Tensor, kv_heads: int, head_dim: int, page_tokens: 
     return pool.numel() * pool.element_size() // size if size else 0
 
 
-def _table(table: torch.Tensor, batch: int):
+def _table(table: torch.Tensor, batch: int, dev: int):
     shape = table.shape
     if len(shape) != 2 or shape[0] != batch:
         raise ValueError("table must be [batch, pages of a sequence]")
-    return _pointer(table, _I32, -1, "table"), shape[1]
+    return _pointer(table, _I32, -1, "table", dev), shape[1]
 
 
 def sz_cache_page_bytes(head_dim: int, kv_heads: int, page_tokens: int) -> int:
@@ -458,20 +475,21 @@ def sz_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor | N
     """Per-head RMS norm (where a weight is given) and rotation of q [tokens,
     q heads, D] and k [tokens, kv heads, D] into q_out and k_out (which may be
     q and k).  inv_freq: fp32, one frequency per rotated pair."""
-    qp, q_shape, qs = _rows(q, _BF16, "q")
-    kp, k_shape, ks = _rows(k, _BF16, "k")
+    dev, launch = _launch_on(stream)
+    qp, q_shape, qs = _rows(q, _BF16, "q", dev)
+    kp, k_shape, ks = _rows(k, _BF16, "k", dev)
     tokens, q_heads, d = q_shape
     if k_shape[0] != tokens or k_shape[2] != d:
         raise ValueError("q and k must have the same tokens and head dimension")
-    qop, _, qos = _written_rows(q_out, _BF16, q_shape, "q_out")
-    kop, _, kos = _written_rows(k_out, _BF16, k_shape, "k_out")
+    qop, _, qos = _written_rows(q_out, _BF16, q_shape, "q_out", dev)
+    kop, _, kos = _written_rows(k_out, _BF16, k_shape, "k_out", dev)
     if (qp == qop and qs != qos) or (kp == kop and ks != kos):
         raise ValueError("an output over its input must have the input's strides")
     _check("sz_qk_norm_rope", _bind.qk_norm_rope(
         _ADDRESS["sz_qk_norm_rope"], qp, qs[0], qs[1], q_heads, kp, ks[0], ks[1], k_shape[1], tokens, d,
-        _pointer(q_weight, _BF16, d, "q_weight"), _pointer(k_weight, _BF16, d, "k_weight"), eps,
-        _pointer(inv_freq, _F32, -1, "inv_freq"), 2 * inv_freq.numel(), interleaved,
-        _pointer(positions, _I32, tokens, "positions"), qop, qos[0], qos[1], kop, kos[0], kos[1], _stream(stream)))
+        _pointer(q_weight, _BF16, d, "q_weight", dev), _pointer(k_weight, _BF16, d, "k_weight", dev), eps,
+        _pointer(inv_freq, _F32, -1, "inv_freq", dev), 2 * inv_freq.numel(), interleaved,
+        _pointer(positions, _I32, tokens, "positions", dev), qop, qos[0], qos[1], kop, kos[0], kos[1], launch))
 
 
 def sz_cache_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, pool: torch.Tensor, page_tokens: int,
@@ -480,8 +498,9 @@ def sz_cache_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, pool:
     """Quantises k and v [tokens, kv heads, D] into the pool at `slots` (int64,
     page * page_tokens + offset; -1 leaves a token out).  weight (fp32) and pos
     (int32), one entry per page, kv head and offset, are set at those slots."""
-    kp, shape, ks = _rows(k, _BF16, "k")
-    vp, v_shape, vs = _rows(v, _BF16, "v")
+    dev, launch = _launch_on(stream)
+    kp, shape, ks = _rows(k, _BF16, "k", dev)
+    vp, v_shape, vs = _rows(v, _BF16, "v", dev)
     if v_shape != shape:
         raise ValueError("k and v must have the same shape")
     if pos is not None and positions is None:
@@ -490,22 +509,23 @@ def sz_cache_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, pool:
     pages = _cache_pages(pool, heads, d, page_tokens)
     cells = pages * heads * page_tokens
     _check("sz_cache_append", _bind.cache_append(
-        _ADDRESS["sz_cache_append"], kp, ks[0], ks[1], vp, vs[0], vs[1], tokens, _pointer(slots, _I64, tokens, "slots"),
-        _pointer(positions, _I32, tokens, "positions"), _pointer(pool, None, -1, "pool"), pages, heads, d, page_tokens,
-        _pointer(weight, _F32, cells, "weight"), _pointer(pos, _I32, cells, "pos"), _pointer(status, _I32, 1, "status"),
-        _stream(stream)))
+        _ADDRESS["sz_cache_append"], kp, ks[0], ks[1], vp, vs[0], vs[1], tokens,
+        _pointer(slots, _I64, tokens, "slots", dev), _pointer(positions, _I32, tokens, "positions", dev),
+        _pointer(pool, None, -1, "pool", dev), pages, heads, d, page_tokens, _pointer(weight, _F32, cells, "weight", dev),
+        _pointer(pos, _I32, cells, "pos", dev), _pointer(status, _I32, 1, "status", dev), launch))
 
 
 def sz_cache_read(pool: torch.Tensor, page_tokens: int, slots: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
                   status: torch.Tensor | None = None, stream=None) -> None:
     """Reads the values at `slots` into k and v [tokens, kv heads, D] as bf16."""
-    kp, shape, ks = _written_rows(k, _BF16, k.shape, "k")
-    vp, _, vs = _written_rows(v, _BF16, shape, "v")
+    dev, launch = _launch_on(stream)
+    kp, shape, ks = _written_rows(k, _BF16, k.shape, "k", dev)
+    vp, _, vs = _written_rows(v, _BF16, shape, "v", dev)
     tokens, heads, d = shape
     _check("sz_cache_read", _bind.cache_read(
-        _ADDRESS["sz_cache_read"], _pointer(pool, None, -1, "pool"), _cache_pages(pool, heads, d, page_tokens), heads, d,
-        page_tokens, _pointer(slots, _I64, tokens, "slots"), tokens, kp, ks[0], ks[1], vp, vs[0], vs[1],
-        _pointer(status, _I32, 1, "status"), _stream(stream)))
+        _ADDRESS["sz_cache_read"], _pointer(pool, None, -1, "pool", dev), _cache_pages(pool, heads, d, page_tokens), heads,
+        d, page_tokens, _pointer(slots, _I64, tokens, "slots", dev), tokens, kp, ks[0], ks[1], vp, vs[0], vs[1],
+        _pointer(status, _I32, 1, "status", dev), launch))
 
 
 def sz_cache_attend_workspace_size(batch: int, q_heads: int, kv_heads: int, head_dim: int, max_tokens: int,
@@ -531,19 +551,20 @@ def sz_debug_attend_stalled(q, pool, kv_heads: int, page_tokens: int, table, len
 
 
 def _attend(name, q, pool, kv_heads, page_tokens, table, lens, scale, out, ws, lse, weight, status, stream) -> None:
-    qp, shape, qs = _rows(q, _BF16, "q")
+    dev, launch = _launch_on(stream)
+    qp, shape, qs = _rows(q, _BF16, "q", dev)
     batch, q_heads, d = shape
-    op, _, os = _written_rows(out, _BF16, shape, "out")
+    op, _, os = _written_rows(out, _BF16, shape, "out", dev)
     if qp == op and batch:
         raise ValueError("out must not be q")
     pages = _cache_pages(pool, kv_heads, d, page_tokens)
-    table_ptr, width = _table(table, batch)
+    table_ptr, width = _table(table, batch, dev)
     _check(name, _bind.cache_attend(
-        _ADDRESS[name], qp, qs[0], qs[1], batch, q_heads, _pointer(pool, None, -1, "pool"), pages, kv_heads,
-        d, page_tokens, table_ptr, width, _pointer(lens, _I32, batch, "lens"), scale, op, os[0], os[1],
-        _pointer(lse, _F32, batch * q_heads, "lse"), _pointer(weight, _F32, pages * kv_heads * page_tokens, "weight"),
-        _pointer(status, _I32, 1, "status"), _pointer(ws, None, -1, "ws"), ws.numel() * ws.element_size(),
-        _stream(stream)))
+        _ADDRESS[name], qp, qs[0], qs[1], batch, q_heads, _pointer(pool, None, -1, "pool", dev), pages, kv_heads,
+        d, page_tokens, table_ptr, width, _pointer(lens, _I32, batch, "lens", dev), scale, op, os[0], os[1],
+        _pointer(lse, _F32, batch * q_heads, "lse", dev),
+        _pointer(weight, _F32, pages * kv_heads * page_tokens, "weight", dev), _pointer(status, _I32, 1, "status", dev),
+        _pointer(ws, None, -1, "ws", dev), ws.numel() * ws.element_size(), launch))
 
 
 def sz_cache_evict_workspace_size(batch: int, kv_heads: int, max_tokens: int) -> int:
@@ -556,15 +577,16 @@ def sz_cache_evict(pool: torch.Tensor, kv_heads: int, head_dim: int, page_tokens
                    stream=None) -> None:
     """Cuts every sequence longer than `keep` to its `keep` most wanted tokens
     per kv head, in place; new_lens gets the lengths left."""
+    dev, launch = _launch_on(stream)
     batch = lens.numel()
     pages = _cache_pages(pool, kv_heads, head_dim, page_tokens)
     cells = pages * kv_heads * page_tokens
-    table_ptr, width = _table(table, batch)
+    table_ptr, width = _table(table, batch, dev)
     if keep < 0 or recent < 0:
         raise ValueError("keep and recent must not be negative")
     _check("sz_cache_evict", _bind.cache_evict(
-        _ADDRESS["sz_cache_evict"], _pointer(pool, None, -1, "pool"), pages, kv_heads, head_dim, page_tokens, table_ptr,
-        width, _pointer(lens, _I32, batch, "lens"), _pointer(next_pos, _I32, batch, "next_pos"), batch, keep, recent,
-        _pointer(weight, _F32, cells, "weight"), _pointer(pos, _I32, cells, "pos"),
-        _pointer(new_lens, _I32, batch, "new_lens"), _pointer(status, _I32, 1, "status"), _pointer(ws, None, -1, "ws"),
-        ws.numel() * ws.element_size(), _stream(stream)))
+        _ADDRESS["sz_cache_evict"], _pointer(pool, None, -1, "pool", dev), pages, kv_heads, head_dim, page_tokens, table_ptr,
+        width, _pointer(lens, _I32, batch, "lens", dev), _pointer(next_pos, _I32, batch, "next_pos", dev), batch, keep, recent,
+        _pointer(weight, _F32, cells, "weight", dev), _pointer(pos, _I32, cells, "pos", dev),
+        _pointer(new_lens, _I32, batch, "new_lens", dev), _pointer(status, _I32, 1, "status", dev),
+        _pointer(ws, None, -1, "ws", dev), ws.numel() * ws.element_size(), launch))

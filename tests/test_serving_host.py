@@ -1,9 +1,10 @@
 """The serving operators on a host without a GPU: what their binding and the
 library refuse before anything is launched."""
 import pytest
+import torch
 
 from tests.test_attend_host import ATTEND
-from tests.test_cache_host import POOL, call
+from tests.test_cache_host import FAKE, POOL, Recorder, call
 
 
 @pytest.fixture(scope="module")
@@ -17,3 +18,115 @@ def S():
 def test_the_stalled_attention_refuses_what_the_attention_does(S, change):
     stalled = {**ATTEND, "status": ATTEND["lens"]}
     assert call(S.LIB, "sz_debug_attend_stalled", stalled, **change) == S.SZ_ERR_INVALID_ARG
+
+
+class OnGpu(torch.Tensor):
+    """A tensor without storage that says it is on the GPU of that number."""
+    is_cuda = True
+    gpu = 0
+
+    def data_ptr(self):
+        return FAKE
+
+    def get_device(self):
+        return self.gpu
+
+
+def on_gpu(*shape, dtype=torch.bfloat16, gpu=0):
+    t = torch.empty(*shape, dtype=dtype, device="meta").as_subclass(OnGpu)
+    t.gpu = gpu
+    return t
+
+
+def stream(gpu):
+    return type("Stream", (), {"cuda_stream": 0, "device_index": gpu})()
+
+
+def calls(S):
+    """Every operator's tensor arguments and a call with them."""
+    i32, i64, f32, u8 = torch.int32, torch.int64, torch.float32, torch.uint8
+    t = on_gpu
+    out = t(4, 8, 128)
+    out.data_ptr = lambda: 2 * FAKE
+    pool, cells = t(9, S.sz_cache_page_bytes(128, 2, 16), dtype=u8), (9, 2, 16)
+    norm = dict(q=t(4, 8, 128), k=t(4, 2, 128), q_weight=t(128), k_weight=t(128), inv_freq=t(64, dtype=f32),
+                positions=t(4, dtype=i32), q_out=t(4, 8, 128), k_out=t(4, 2, 128))
+    rows = dict(k=t(4, 2, 128), v=t(4, 2, 128), slots=t(4, dtype=i64), pool=pool, status=t(1, dtype=i32))
+    tables = dict(weight=t(*cells, dtype=f32), pos=t(*cells, dtype=i32))
+    append = {**rows, **tables, "positions": t(4, dtype=i32)}
+    lists = dict(pool=pool, table=t(4, 3, dtype=i32), lens=t(4, dtype=i32), ws=t(8, dtype=u8), status=t(1, dtype=i32))
+    attend = {**lists, "q": t(4, 8, 128), "out": out, "lse": t(4, 8, dtype=f32), "weight": tables["weight"]}
+    evict = {**lists, **tables, "next_pos": t(4, dtype=i32), "new_lens": t(4, dtype=i32)}
+    return [(norm, lambda **a: S.sz_qk_norm_rope(eps=1e-6, **a)), (append, lambda **a: S.sz_cache_append(page_tokens=16, **a)),
+            (rows, lambda **a: S.sz_cache_read(page_tokens=16, **a)),
+            (attend, lambda **a: S.sz_cache_attend(kv_heads=2, page_tokens=16, scale=0.1, **a)),
+            (evict, lambda **a: S.sz_cache_evict(kv_heads=2, head_dim=128, page_tokens=16, keep=8, recent=2, **a))]
+
+
+def test_tensors_of_another_gpu_are_refused(S, monkeypatch):
+    """A kernel runs on the current GPU and would follow a pointer into another
+    one; no call is made with such a tensor, nor on another GPU's stream."""
+    rec = Recorder(S._bind)
+    monkeypatch.setattr(S, "_bind", rec)
+    current = 0
+    monkeypatch.setattr(S.torch.cuda, "current_device", lambda: current)
+    monkeypatch.setattr(S, "_get_device", lambda: current)
+    monkeypatch.setattr(S, "_raw_stream", lambda device: 1000 + device)
+    for args, f in calls(S):
+        for given in (None, stream(0)):
+            f(**args, stream=given)
+        assert len(rec.calls) == 2
+        del rec.calls[:]
+        for name, t in args.items():
+            for given in (None, stream(0)):
+                other = t.as_subclass(OnGpu)
+                other.gpu = 1
+                other.data_ptr = t.data_ptr
+                with pytest.raises(ValueError, match=name + ".* GPU"):
+                    f(**{**args, name: other}, stream=given)
+                other.gpu = -1
+                with pytest.raises(ValueError, match=name):
+                    f(**{**args, name: other}, stream=given)
+        with pytest.raises(ValueError, match="stream"):
+            f(**args, stream=stream(1))
+        current = 1
+        with pytest.raises(ValueError, match="GPU"):
+            f(**args, stream=None)
+        current = 0
+        assert rec.calls == []
+
+
+def test_a_cache_runs_on_its_own_gpu(S, monkeypatch):
+    """Every method of a DecodeCache makes the cache's GPU the current one."""
+    from lossless_kv_cache_bf16_gb300 import decode
+
+    current, used = [0], []
+
+    class Device:
+        def __init__(self, device):
+            self.index = device.index
+
+        def __enter__(self):
+            current.append(self.index)
+
+        def __exit__(self, *_):
+            current.pop()
+
+    for name in ("sz_qk_norm_rope", "sz_cache_append", "sz_cache_attend", "sz_cache_evict", "sz_decode"):
+        monkeypatch.setattr(decode.S, name, lambda *a, name=name, **k: used.append((name, current[-1])))
+    monkeypatch.setattr(decode.torch.cuda, "device", Device)
+    cache = decode.DecodeCache(1, 4, 2, 64, 64, page_tokens=16, budget=16, device="cpu")
+    rows = torch.zeros(3, 2, 64, dtype=torch.bfloat16)
+    gpu1 = type("Gpu", (), {"type": "cuda", "index": 1})()
+    cache._gpu = lambda: Device(gpu1)
+    cache.extend(0, rows, rows)
+    cache.extend_from_stream(0, torch.zeros(8, dtype=torch.uint8), 8, 2)
+    for _ in range(40):
+        cache.step(torch.zeros(1, 8, 64, dtype=torch.bfloat16), None, None, torch.ones(32))
+    assert {name for name, _ in used} == {"sz_qk_norm_rope", "sz_cache_append", "sz_cache_attend", "sz_cache_evict", "sz_decode"}
+    assert {gpu for _, gpu in used} == {1} and current == [0]
+    with pytest.raises(ValueError, match="GPU"):
+        cache.extend_from_stream(0, torch.zeros(8, dtype=torch.uint8, device="meta"), 8, 2)
+    cache = decode.DecodeCache(1, 4, 2, 64, 64, page_tokens=16, device="cpu")
+    cache.device = torch.device("cuda:1")
+    assert cache._gpu().index == 1
