@@ -300,6 +300,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attend_kernel(const
     const uint8_t* src = nullptr;
     uint32_t tokens = 0, batch_mask = 0, batch_units = 0, batch_at = 0;
     uint32_t in_flight = 0;  // stages issued and not yet waited for
+    bool left_out = false;   // tokens of pages outside the pool: without any, no item is empty
     auto look_up = [&]() {
         batch_at = batch_units = 0;
         settle();
@@ -308,7 +309,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attend_kernel(const
         const uint32_t first = (nxt.at - kItemCost) * kUnitTokens + lane * kCellTokens;
         const uint32_t len = s_len[nxt.b];
         tokens = 0;
-        if (lane < 2 * batch_units && first < len) {
+        const bool held = lane < 2 * batch_units && first < len;
+        if (held) {
             const int32_t page = p.table[(uint64_t)nxt.b * p.table_width + (first >> lg_page)];
             if ((uint32_t)page < p.pool.pages) {
                 tokens = min(len - first, kCellTokens);
@@ -319,6 +321,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attend_kernel(const
             }
         }
         batch_mask = __ballot_sync(0xFFFFFFFFu, tokens != 0);
+        left_out |= __any_sync(0xFFFFFFFFu, held && tokens == 0);
         nxt.at += batch_units;
         nxt_left -= batch_units;
     };
@@ -364,7 +367,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attend_kernel(const
     for (int k = 0; k < Sh::kStages; k++) issue(k);
     const uint32_t half_sel = g & 1u ? 0x3244u : 0x1044u;  // scales come in pairs of tokens
     uint32_t stage = 0, phase = 0;
-    bool alive = true;  // false once a wait has given up: the rest is left out
+    // 0 once a wait has given up: the rest is left out.  -1: the first will.
+    int alive = blockIdx.x == p.stalled_block ? -1 : 1;
 
     for (uint32_t left = n_run; left;) {
         const uint32_t cost = entries(s_len[cur.b]), take = min(left, cost - cur.at);
@@ -431,7 +435,6 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attend_kernel(const
 
         float o[NT][2 * kG][4];
         float m[NT][2], l[NT][2];  // of heads 2t and 2t + 1; l: this thread's share of the sum of weights
-        uint32_t seen = 0;         // not 0 once there was a token
 #pragma unroll
         for (int n = 0; n < NT; n++) {
             m[n][0] = m[n][1] = kNegInf;
@@ -445,8 +448,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attend_kernel(const
 #pragma unroll 1
         for (uint32_t unit = r0; unit < r1; unit++) {
             if (alive) {
-                alive = __all_sync(0xFFFFFFFFu,
-                                   blockIdx.x != p.stalled_block && mbar_wait(&bars[stage], phase, p.wait_limit_ns));
+                alive = __all_sync(0xFFFFFFFFu, alive > 0 && mbar_wait(&bars[stage], phase, p.wait_limit_ns));
                 if (!alive) {
                     // The copies still under way must land before the block
                     // gives its shared memory back.
@@ -463,7 +465,6 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attend_kernel(const
             if (!alive) break;
             const uint8_t* u = ring + stage * Sh::kUnitBytes;
             const uint2 held = *reinterpret_cast<const uint2*>(counts + 2 * stage);  // tokens of the two cells
-            seen |= held.x | held.y;
             auto take_unit = [&](auto partial) {
                 constexpr bool PARTIAL = decltype(partial)::value;
                 // S: s[n][c][2 r + k] is token 16 c + 8 r + g, head 8 n + 2 t + k.
@@ -623,7 +624,6 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attend_kernel(const
         // Sums of weights are in units of 2^-92, code sums times 2^-41 (odd
         // channels 2^-37).
         const bool first_piece = !starts;
-        seen |= !alive;
         float* piece = reinterpret_cast<float*>(first_piece ? smem + Sh::kPiece + warp * Sh::kPieceBytes : ring);
         if (!starts || !ends) __syncwarp();
 #pragma unroll
@@ -635,8 +635,9 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attend_kernel(const
                 l[n][k] += __shfl_xor_sync(0xFFFFFFFFu, l[n][k], 16);
                 // A row that lacks tokens for a wait that gave up is NaN.
                 l[n][k] = alive ? l[n][k] * 2.0194839173657902e-28f : __int_as_float(0x7FC00000);
-                // Tokens whose logits are all -infinity are no empty row.
-                if (seen) m[n][k] = fmaxf(m[n][k], -FLT_MAX);
+                // A row without tokens keeps the maximum -infinity; one whose
+                // logits are all -infinity does not.
+                if (!left_out || l[n][k] != 0.f) m[n][k] = fmaxf(m[n][k], -FLT_MAX);
             }
 #pragma unroll
             for (int j = 0; j < 2 * kG; j++) {
@@ -764,6 +765,14 @@ template <int D>
 __global__ void __launch_bounds__(256) attend_join_kernel(const AttendParams p, const uint32_t item_heads) {
     wait_for_previous();
     const int32_t b = p.meta[4 * blockIdx.x];
+    // Whether any block has given up, in the first one's place.  The list ends
+    // in the last block or before, so that it never has an item to join.
+    if (p.weight && blockIdx.x == gridDim.x - 1) {
+        int gave_up = 0;
+        for (uint32_t k = threadIdx.x; k < gridDim.x; k += 256) gave_up |= p.meta[4 * k + 3];
+        gave_up = __syncthreads_or(gave_up);
+        if (threadIdx.x == 0) p.meta[3] = gave_up;
+    }
     if (b < 0) return;
     const uint32_t item = (uint32_t)p.meta[4 * blockIdx.x + 1];
     const int more = p.meta[4 * blockIdx.x + 2];
@@ -805,13 +814,17 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const AttendParams p, 
 // addition per call and sequence; atomic, for pages that two sequences share.
 // Adds nothing where a block of the first kernel has given up: its logits are
 // missing, and the call can be made again with the weights as they were.
-__global__ void __launch_bounds__(256) attend_weight_kernel(const AttendParams p, const uint32_t first_blocks) {
+// flags: how many of meta's blocks say so, 1 where the join has gathered them.
+__global__ void __launch_bounds__(256) attend_weight_kernel(const AttendParams p, const uint32_t flags) {
     wait_for_previous();
-    int gave_up = 0;
-    for (uint32_t k = threadIdx.x; k < first_blocks; k += 256) gave_up |= p.meta[4 * k + 3];
-    if (__syncthreads_or(gave_up)) return;
     const uint32_t b = blockIdx.z, kv_head = blockIdx.y;
     const int32_t len = p.lens[b];
+    // Looked at before the first addition only, behind the loads for it.
+    int gave_up = p.meta[3];
+    if (flags > 1) {
+        for (uint32_t k = threadIdx.x % 32; k < flags; k += 32) gave_up |= p.meta[4 * k + 3];
+        gave_up = __any_sync(0xFFFFFFFFu, gave_up);
+    }
     const uint64_t max_tokens = (uint64_t)p.table_width << p.pool.lg_page;
     if (len <= 0 || (uint64_t)len > max_tokens) return;
     const uint32_t q_heads = p.pool.heads * p.group;
@@ -835,6 +848,7 @@ __global__ void __launch_bounds__(256) attend_weight_kernel(const AttendParams p
                 w[2] += exp2_fast(x[k].z - ref[k]), w[3] += exp2_fast(x[k].w - ref[k]);
             }
         }
+        if (gave_up) return;
         float* dst = p.weight + ((((uint64_t)(uint32_t)page * p.pool.heads + kv_head) << p.pool.lg_page) +
                                  (tok & ((1u << p.pool.lg_page) - 1u)));
         if (p.weight_vec && tok + 4 <= (uint32_t)len) {
@@ -872,7 +886,7 @@ cudaError_t launch(const AttendParams& p, cudaStream_t s) {
     if (err != cudaSuccess || !LOGITS) return err;
     const uint32_t blocks = (uint32_t)((tokens + 1023) / 1024);
     return launch_dependent(attend_weight_kernel, dim3(blocks < 1024 ? blocks : 1024, p.pool.heads, p.batch), dim3(256), 0, s, p,
-                            first_blocks);
+                            q.whole_items ? first_blocks : 1u);
 }
 
 template <int D>
