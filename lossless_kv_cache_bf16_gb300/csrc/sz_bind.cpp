@@ -139,8 +139,30 @@ PyObject* written_rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return got.o;
 }
 
-// pointer(t, dtype or None, count or -1, what[, device]) -> data_ptr of a contiguous CUDA
-// tensor of that type with that many values; None for None.
+// Whether t has the values of a tensor of that shape, in its own shape if it
+// has as many dimensions.  False with an error.
+bool holds(PyObject* t, PyObject* want, PyObject* what) {
+    Ref shape(PyObject_GetAttr(t, s_shape));
+    if (!shape) return false;
+    if (PyTuple_Check(shape.o) && PyTuple_GET_SIZE(shape.o) == PyTuple_GET_SIZE(want)) {
+        const int same = PyObject_RichCompareBool(shape.o, want, Py_EQ);
+        if (same == 0) PyErr_Format(PyExc_ValueError, "%U must have shape %R, not %R", what, want, shape.o);
+        return same > 0;
+    }
+    long long values = 1;
+    for (Py_ssize_t k = 0; k < PyTuple_GET_SIZE(want); k++) values *= PyLong_AsLongLong(PyTuple_GET_ITEM(want, k));
+    Ref numel(PyObject_CallMethodNoArgs(t, s_numel));
+    if (!numel || PyErr_Occurred()) return false;
+    const long long got = PyLong_AsLongLong(numel.o);
+    if (got != values && !PyErr_Occurred())
+        PyErr_Format(PyExc_ValueError, "%U must hold %lld values, not %lld", what, values, got);
+    return got == values;
+}
+
+// pointer(t, dtype or None, count, what[, device]) -> data_ptr of a contiguous
+// CUDA tensor of that type; None for None.  count: its number of values, its
+// shape (a flat tensor, or one of other dimensions, need only hold as many
+// values), or -1.
 PyObject* pointer(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (!expect(n, 4, 1)) return nullptr;
     PyObject *t = a[0], *what = a[3];
@@ -155,7 +177,10 @@ PyObject* pointer(PyObject*, PyObject* const* a, Py_ssize_t n) {
             return nullptr;
         }
     }
-    const long long want = PyLong_AsLongLong(a[2]);
+    if (PyTuple_Check(a[2])) {
+        if (!holds(t, a[2], what)) return nullptr;
+    }
+    const long long want = PyTuple_Check(a[2]) ? -1 : PyLong_AsLongLong(a[2]);
     if (want == -1 && PyErr_Occurred()) return nullptr;
     if (want >= 0) {
         Ref numel(PyObject_CallMethodNoArgs(t, s_numel));

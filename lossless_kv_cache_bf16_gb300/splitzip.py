@@ -447,7 +447,9 @@ _PAGE_BYTES: dict = {}  # (head_dim, kv_heads, page_tokens) -> bytes of a page
 
 
 def _cache_pages(pool: torch.Tensor, kv_heads: int, head_dim: int, page_tokens: int) -> int:
-    """Whole pages that the pool tensor (any dtype) holds."""
+    """Whole pages that the pool tensor (any dtype) holds.  A pool of more than
+    one dimension must have its pages as the leading ones: rows of another
+    number of heads, or another page size, would find other pages in it."""
     size = _PAGE_BYTES.get((head_dim, kv_heads, page_tokens))
     if size is None:
         if min(head_dim, kv_heads, page_tokens) < 0:
@@ -455,7 +457,18 @@ def _cache_pages(pool: torch.Tensor, kv_heads: int, head_dim: int, page_tokens: 
         size = int(LIB.sz_cache_page_bytes(head_dim, kv_heads, page_tokens))
         if size and len(_PAGE_BYTES) < 1024:
             _PAGE_BYTES[(head_dim, kv_heads, page_tokens)] = size
-    return pool.numel() * pool.element_size() // size if size else 0
+    pages = pool.numel() * pool.element_size() // size if size else 0
+    shape = pool.shape
+    if len(shape) > 1 and pages:
+        lead = 1
+        for n in shape[:-1]:
+            lead *= n
+            if lead >= pages:
+                break
+        if lead != pages and lead != 1:
+            raise ValueError(f"pool of shape {tuple(shape)} is not the {pages} pages that {kv_heads} heads of {head_dim} "
+                             f"in pages of {page_tokens} tokens would make of it")
+    return pages
 
 
 def _table(table: torch.Tensor, batch: int, dev: int):
@@ -507,7 +520,7 @@ def sz_cache_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, pool:
         raise ValueError("pos needs positions")
     tokens, heads, d = shape
     pages = _cache_pages(pool, heads, d, page_tokens)
-    cells = pages * heads * page_tokens
+    cells = (pages, heads, page_tokens)
     _check("sz_cache_append", _bind.cache_append(
         _ADDRESS["sz_cache_append"], kp, ks[0], ks[1], vp, vs[0], vs[1], tokens,
         _pointer(slots, _I64, tokens, "slots", dev), _pointer(positions, _I32, tokens, "positions", dev),
@@ -563,7 +576,7 @@ def _attend(name, q, pool, kv_heads, page_tokens, table, lens, scale, out, ws, l
         _ADDRESS[name], qp, qs[0], qs[1], batch, q_heads, _pointer(pool, None, -1, "pool", dev), pages, kv_heads,
         d, page_tokens, table_ptr, width, _pointer(lens, _I32, batch, "lens", dev), scale, op, os[0], os[1],
         _pointer(lse, _F32, batch * q_heads, "lse", dev),
-        _pointer(weight, _F32, pages * kv_heads * page_tokens, "weight", dev), _pointer(status, _I32, 1, "status", dev),
+        _pointer(weight, _F32, (pages, kv_heads, page_tokens), "weight", dev), _pointer(status, _I32, 1, "status", dev),
         _pointer(ws, None, -1, "ws", dev), ws.numel() * ws.element_size(), launch))
 
 
@@ -580,7 +593,7 @@ def sz_cache_evict(pool: torch.Tensor, kv_heads: int, head_dim: int, page_tokens
     dev, launch = _launch_on(stream)
     batch = lens.numel()
     pages = _cache_pages(pool, kv_heads, head_dim, page_tokens)
-    cells = pages * kv_heads * page_tokens
+    cells = (pages, kv_heads, page_tokens)
     table_ptr, width = _table(table, batch, dev)
     if keep < 0 or recent < 0:
         raise ValueError("keep and recent must not be negative")

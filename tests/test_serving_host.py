@@ -130,3 +130,46 @@ def test_a_cache_runs_on_its_own_gpu(S, monkeypatch):
     cache = decode.DecodeCache(1, 4, 2, 64, 64, page_tokens=16, device="cpu")
     cache.device = torch.device("cuda:1")
     assert cache._gpu().index == 1
+
+
+def test_rows_of_another_head_count_than_the_pools_are_refused(S, monkeypatch):
+    """A pool's bytes make whole pages for other head counts and page sizes
+    too; its shape, and the tables', say which ones are meant."""
+    rec = Recorder(S._bind)
+    monkeypatch.setattr(S, "_bind", rec)
+    f32, i32, u8 = torch.float32, torch.int32, torch.uint8
+    t, pages, heads, page = on_gpu, 20, 8, 16
+    size = S.sz_cache_page_bytes(128, heads, page)
+    table = lambda *shape: (t(*shape, dtype=f32), t(*shape, dtype=i32))
+
+    def append(pool, rows=heads, page=page, weight=None, pos=None):
+        S.sz_cache_append(t(4, rows, 128), t(4, rows, 128), t(4, dtype=torch.int64), pool, page, positions=t(4, dtype=i32),
+                          weight=weight, pos=pos, stream=stream(-1))
+
+    weight, pos = table(pages, heads, page)
+    good = [t(pages, size, dtype=u8), t(pages, heads, size // heads, dtype=u8), t(pages * size, dtype=u8),
+            t(1, pages * size, dtype=u8), t(4, 5, size, dtype=u8), t(pages, size // 2), t(1, pages, size, dtype=u8)]
+    for pool in good:
+        append(pool)
+        append(pool, weight=weight, pos=pos)
+        flat = table(pages * heads * page)
+        append(pool, weight=flat[0], pos=flat[1])
+    assert rec.calls == ["cache_append"] * 3 * len(good)
+    del rec.calls[:]
+    for rows, other in ((4, page), (2, page), (16, page), (heads, 32)):
+        for pool in (good[0], good[1], good[4], good[5], good[6]):
+            with pytest.raises(ValueError, match="pool"):
+                append(pool, rows, other)
+    flat = good[2]
+    for rows, other in ((4, page), (2, page), (16, page), (1, 128)):
+        with pytest.raises(ValueError, match="weight"):
+            append(flat, rows, other, weight=weight)
+        with pytest.raises(ValueError, match="pos"):
+            append(flat, rows, other, pos=pos)
+    for bad in ((heads, pages, page), (pages, page, heads), (pages, heads, page + 1), (pages * heads * page + 1,)):
+        weight, pos = table(*bad)
+        with pytest.raises(ValueError, match="weight"):
+            append(good[0], weight=weight)
+        with pytest.raises(ValueError, match="pos"):
+            append(good[0], pos=pos)
+    assert rec.calls == []
