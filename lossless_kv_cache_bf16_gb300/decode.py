@@ -73,6 +73,9 @@ class DecodeCache:
     @_on_its_gpu
     def extend(self, sequence: int, k: torch.Tensor, v: torch.Tensor) -> None:
         """Appends a prompt's rows [tokens, kv heads, D], keys already rotated."""
+        row = (self.kv_heads, self.head_dim)
+        if k.dim() != 3 or k.shape[1:] != row or v.shape != k.shape:
+            raise ValueError(f"k and v must be [tokens, {self.kv_heads}, {self.head_dim}], not {tuple(k.shape)} and {tuple(v.shape)}")
         n, at = k.shape[0], self.held[sequence]
         if at + n > self.capacity:
             raise ValueError(f"{at + n} tokens do not fit in {self.capacity}")
@@ -106,9 +109,11 @@ class DecodeCache:
              out: torch.Tensor | None = None) -> torch.Tensor:
         """One token of every sequence: qkv [batch, q heads + 2 kv heads, D] as
         a layer's projection gives it; returns the attention [batch, q heads, D]."""
+        hq, hk = self.q_heads, self.kv_heads
+        if qkv.shape != (self.batch, hq + 2 * hk, self.head_dim):
+            raise ValueError(f"qkv must be {[self.batch, hq + 2 * hk, self.head_dim]}, not {list(qkv.shape)}")
         if max(self.held) + 1 > self.capacity:
             raise ValueError("the cache is full")
-        hq, hk = self.q_heads, self.kv_heads
         q, k, v = qkv[:, :hq], qkv[:, hq:hq + hk], qkv[:, hq + hk:]
         S.sz_qk_norm_rope(q, k, q_weight, k_weight, eps, inv_freq, self.next_pos, q, k)
         at = self.lens.long()

@@ -173,3 +173,34 @@ def test_rows_of_another_head_count_than_the_pools_are_refused(S, monkeypatch):
         with pytest.raises(ValueError, match="pos"):
             append(good[0], pos=pos)
     assert rec.calls == []
+
+
+@pytest.fixture
+def cache(S, monkeypatch):
+    """A DecodeCache without a GPU, whose calls are recorded."""
+    from lossless_kv_cache_bf16_gb300 import decode
+
+    made = []
+    for name in ("sz_qk_norm_rope", "sz_cache_append", "sz_cache_attend", "sz_cache_evict", "sz_decode"):
+        monkeypatch.setattr(decode.S, name, lambda *a, name=name, **k: made.append(name))
+    cache = decode.DecodeCache(2, 4, 2, 64, 64, page_tokens=16, budget=16, recent=4, device="cpu")
+    cache.calls = made
+    return cache
+
+
+def bf16(*shape):
+    return torch.zeros(*shape, dtype=torch.bfloat16)
+
+
+def test_a_cache_refuses_rows_that_are_not_its_own(cache):
+    state = lambda: (cache.lens.tolist(), cache.next_pos.tolist(), list(cache.held))
+    before = state()
+    for k, v in ((bf16(3, 4, 64), bf16(3, 4, 64)), (bf16(3, 1, 64), bf16(3, 1, 64)), (bf16(3, 2, 128), bf16(3, 2, 128)),
+                 (bf16(3, 2, 64), bf16(4, 2, 64)), (bf16(3, 2, 64), bf16(3, 1, 64)), (bf16(6, 64), bf16(6, 64))):
+        with pytest.raises(ValueError):
+            cache.extend(0, k, v)
+    freq = torch.ones(32)
+    for qkv in (bf16(2, 7, 64), bf16(1, 8, 64), bf16(2, 8, 128), bf16(2, 512), bf16(2, 12, 64)):
+        with pytest.raises(ValueError):
+            cache.step(qkv, None, None, freq)
+    assert cache.calls == [] and state() == before
