@@ -443,22 +443,22 @@ def _launch_on(stream):
     return device, stream.cuda_stream
 
 
-_PAGE_BYTES: dict = {}  # (head_dim, kv_heads, page_tokens) -> bytes of a page
+_PAGES: dict = {}  # (pool shape, its type, head_dim, kv_heads, page_tokens) -> whole pages
 
 
 def _cache_pages(pool: torch.Tensor, kv_heads: int, head_dim: int, page_tokens: int) -> int:
     """Whole pages that the pool tensor (any dtype) holds.  A pool of more than
     one dimension must have its pages as the leading ones: rows of another
     number of heads, or another page size, would find other pages in it."""
-    size = _PAGE_BYTES.get((head_dim, kv_heads, page_tokens))
-    if size is None:
-        if min(head_dim, kv_heads, page_tokens) < 0:
-            raise ValueError("sizes must not be negative")
-        size = int(LIB.sz_cache_page_bytes(head_dim, kv_heads, page_tokens))
-        if size and len(_PAGE_BYTES) < 1024:
-            _PAGE_BYTES[(head_dim, kv_heads, page_tokens)] = size
-    pages = pool.numel() * pool.element_size() // size if size else 0
     shape = pool.shape
+    key = (shape, pool.dtype, head_dim, kv_heads, page_tokens)
+    pages = _PAGES.get(key)
+    if pages is not None:
+        return pages
+    if min(head_dim, kv_heads, page_tokens) < 0:
+        raise ValueError("sizes must not be negative")
+    size = int(LIB.sz_cache_page_bytes(head_dim, kv_heads, page_tokens))
+    pages = pool.numel() * pool.element_size() // size if size else 0
     if len(shape) > 1 and pages:
         lead = 1
         for n in shape[:-1]:
@@ -468,6 +468,8 @@ def _cache_pages(pool: torch.Tensor, kv_heads: int, head_dim: int, page_tokens: 
         if lead != pages and lead != 1:
             raise ValueError(f"pool of shape {tuple(shape)} is not the {pages} pages that {kv_heads} heads of {head_dim} "
                              f"in pages of {page_tokens} tokens would make of it")
+    if len(_PAGES) < 1024:
+        _PAGES[key] = pages
     return pages
 
 
