@@ -414,7 +414,8 @@ size_t sz_cache_page_bytes(size_t head_dim, size_t kv_heads, size_t page_tokens)
  *                      normalised only
  *  d_inv_freq          rot_dim / 2 floats
  *  d_positions         one int32 per token
- *  d_q_out, d_k_out    may be the inputs (with the same strides)
+ *  d_q_out, d_k_out    may be the inputs (with the same strides); an output
+ *                      that shares memory with other rows is refused
  * Asynchronous. */
 sz_status sz_qk_norm_rope(const void* d_q, int64_t q_token_stride, int64_t q_head_stride, size_t q_heads,
                           const void* d_k, int64_t k_token_stride, int64_t k_head_stride, size_t kv_heads,
@@ -443,7 +444,8 @@ sz_status sz_cache_append(const void* d_k, int64_t k_token_stride, int64_t k_hea
                           cudaStream_t stream);
 
 /* The values that the cache holds at d_slots, rounded to bfloat16; rows of
- * slot -1 and of slots outside the pool (reported) are zero. */
+ * slot -1 and of slots outside the pool (reported) are zero.  Rows of d_k and
+ * d_v that share memory are refused. */
 sz_status sz_cache_read(const void* d_pool, size_t pool_pages, size_t kv_heads, size_t head_dim, size_t page_tokens,
                         const int64_t* d_slots, size_t tokens, void* d_k, int64_t k_token_stride,
                         int64_t k_head_stride, void* d_v, int64_t v_token_stride, int64_t v_head_stride,
@@ -460,7 +462,7 @@ size_t sz_cache_attend_workspace_size(size_t batch, size_t q_heads, size_t kv_he
  * scale * q K^T) V with q_heads / kv_heads (1 .. 1024) consecutive query heads
  * per kv head.
  *  d_q, d_out   [batch][q_heads][head_dim] by their strides, batch <= 2048;
- *               they must not overlap
+ *               refused where rows of the two share memory
  *  d_table      int32 [batch][table_width] page ids; table_width * page_tokens
  *               < 2^31.  Entries past a sequence's length are not read
  *  d_lens       int32 tokens per sequence.  An empty sequence gives zero rows

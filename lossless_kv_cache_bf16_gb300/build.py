@@ -77,7 +77,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     def compile_binding():
         part = BINDING + f".{os.getpid()}.part"
         cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-Wall", "-shared", "-fPIC", "-fvisibility=hidden",
-               f"-I{sysconfig.get_paths()['include']}", f"-I{INCLUDE}",
+               f"-I{sysconfig.get_paths()['include']}", f"-I{INCLUDE}", f"-I{CSRC}",
                f"-I{os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(exe))), 'include')}",
                os.path.join(CSRC, "sz_bind.cpp"), "-o", part]
         res = subprocess.run(cmd, capture_output=True, text=True)

@@ -13,6 +13,7 @@
 #include <cstring>
 
 #include "splitzip.h"
+#include "sz_rows.h"
 
 namespace {
 
@@ -137,6 +138,26 @@ PyObject* written_rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     Py_INCREF(got.o);
     return got.o;
+}
+
+// overlap(a, b): whether two results of rows() or written_rows() share memory.
+PyObject* overlap(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    if (!expect(n, 2)) return nullptr;
+    sz::RowSet set[2];
+    uint64_t dim = 0;
+    for (int k = 0; k < 2; k++) {
+        PyObject *ptr, *shape, *stride;
+        unsigned long long size[3];
+        long long step[3];
+        if (!PyArg_ParseTuple(a[k], "OO!O!", &ptr, &PyTuple_Type, &shape, &PyTuple_Type, &stride) ||
+            !PyArg_ParseTuple(shape, "KKK", &size[0], &size[1], &size[2]) ||
+            !PyArg_ParseTuple(stride, "LLL", &step[0], &step[1], &step[2]))
+            return nullptr;
+        set[k] = {PyLong_AsVoidPtr(ptr), step[0], step[1], size[0], size[1]};
+        if (PyErr_Occurred()) return nullptr;
+        dim = k == 0 || size[2] > dim ? size[2] : dim;
+    }
+    return PyBool_FromLong(sz::rows_overlap(set[0], set[1], dim));
 }
 
 // Whether t has the values of a tensor of that shape, in its own shape if it
@@ -271,7 +292,7 @@ PyObject* cache_evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 #define FAST(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(name)), METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {FAST(rows),        FAST(written_rows), FAST(pointer),      FAST(qk_norm_rope), FAST(cache_append),
+PyMethodDef methods[] = {FAST(rows),        FAST(written_rows), FAST(overlap),      FAST(pointer),      FAST(qk_norm_rope), FAST(cache_append),
                          FAST(cache_read),  FAST(cache_attend), FAST(cache_evict),  {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_sz_bind", "Checks and calls of splitzip.py's serving operators.", -1, methods,

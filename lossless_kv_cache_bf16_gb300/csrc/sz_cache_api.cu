@@ -8,6 +8,7 @@
 #include "splitzip.h"
 #include "sz_cache.h"
 #include "sz_params.h"
+#include "sz_rows.h"
 
 namespace {
 
@@ -125,6 +126,9 @@ sz_status attend(const char* name, uint32_t stalled_block, const void* d_q, int6
                       !aligned(d_ws, 256)))
         return SZ_ERR_INVALID_ARG;
     if (batch == 0) return clear_status(d_status, stream);
+    if (rows_overlap({d_out, out_seq_stride, out_head_stride, batch, q_heads}, {d_q, q_seq_stride, q_head_stride, batch, q_heads},
+                     head_dim))
+        return SZ_ERR_INVALID_ARG;
     uint32_t item_heads = 0, blocks = 0;
     const uint32_t group = (uint32_t)(q_heads / kv_heads);
     const cudaError_t err = attend_shape(group, &item_heads, &blocks);
@@ -203,6 +207,17 @@ sz_status sz_qk_norm_rope(const void* d_q, int64_t q_token_stride, int64_t q_hea
         p.vec &= aligned(in[w], 16) && aligned(out[w], 16) && aligned(weight[w], 16) &&
                  multiple(strides[w][0], strides[w][1], 8) && multiple(strides[w][2], strides[w][3], 8);
     }
+    // An output may be its input; no other rows may share memory with one.
+    RowSet src[2], dst[2];
+    for (int w = 0; w < 2; w++) {
+        src[w] = {in[w], strides[w][0], strides[w][1], tokens, heads[w]};
+        dst[w] = {out[w], strides[w][2], strides[w][3], tokens, heads[w]};
+    }
+    for (int w = 0; w < 2; w++) {
+        if (!same_rows(dst[w], src[w]) && rows_overlap(dst[w], src[w], head_dim)) return SZ_ERR_INVALID_ARG;
+        if (rows_overlap(dst[w], src[1 - w], head_dim)) return SZ_ERR_INVALID_ARG;
+    }
+    if (rows_overlap(dst[0], dst[1], head_dim)) return SZ_ERR_INVALID_ARG;
     p.inv_freq = d_inv_freq;
     p.positions = d_positions;
     p.tokens = (uint32_t)tokens;
@@ -241,6 +256,9 @@ sz_status sz_cache_read(const void* d_pool, size_t pool_pages, size_t kv_heads, 
     AppendParams p{};
     if (!pool_for(d_pool, pool_pages, kv_heads, head_dim, page_tokens, &p.pool)) return SZ_ERR_INVALID_ARG;
     if (!rows_for(d_k, k_token_stride, k_head_stride, d_v, v_token_stride, v_head_stride, d_slots, tokens, d_status, &p))
+        return SZ_ERR_INVALID_ARG;
+    if (rows_overlap({d_k, k_token_stride, k_head_stride, tokens, kv_heads}, {d_v, v_token_stride, v_head_stride, tokens, kv_heads},
+                     head_dim))
         return SZ_ERR_INVALID_ARG;
     const sz_status st = clear_status(d_status, stream);
     if (st != SZ_OK || tokens == 0) return st;

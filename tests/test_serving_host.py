@@ -1,10 +1,12 @@
 """The serving operators on a host without a GPU: what their binding and the
 library refuse before anything is launched."""
+import random
+
 import pytest
 import torch
 
 from tests.test_attend_host import ATTEND
-from tests.test_cache_host import FAKE, POOL, Recorder, call
+from tests.test_cache_host import FAKE, NORM, POOL, READ, Recorder, call
 
 
 @pytest.fixture(scope="module")
@@ -204,3 +206,50 @@ def test_a_cache_refuses_rows_that_are_not_its_own(cache):
         with pytest.raises(ValueError):
             cache.step(qkv, None, None, freq)
     assert cache.calls == [] and state() == before
+
+
+def test_overlap_of_rows_against_every_byte(S):
+    """overlap() against the sets of elements, for views of one small buffer."""
+    rng = random.Random(7)
+    room = torch.zeros(400, dtype=torch.bfloat16)
+    found = [0, 0]
+    for _ in range(4000):
+        dim = rng.choice([1, 2, 8])
+        strides = (rng.choice([0, 1, 3, 8, 12, 24, 40]), rng.choice([0, 1, 5, 8, 16, 48]))
+
+        def view():
+            size = (rng.randrange(0, 5), rng.randrange(0, 4), dim)
+            step = (*(s if rng.random() < 0.9 else rng.choice([2, 8, 30]) for s in strides), 1)
+            at = rng.randrange(0, 40)
+            t = room.as_strided(size, step, at)
+            hit = {at + i * step[0] + j * step[1] + c for i in range(size[0]) for j in range(size[1]) for c in range(dim)}
+            return (t.data_ptr() or room.data_ptr(), size, step), hit
+
+        (a, in_a), (b, in_b) = view(), view()
+        got, want = S._bind.overlap(a, b), bool(in_a & in_b)
+        assert got == S._bind.overlap(b, a)
+        common = all(a[1][k] <= 1 or b[1][k] <= 1 or a[2][k] == b[2][k] for k in range(2))
+        if common or want:
+            assert got == want, (a, b)
+            found[want] += 1
+    assert min(found) > 500
+
+
+def test_rows_that_share_memory_with_an_output_are_refused(S):
+    """Views of one packed buffer (8 query, 2 key and 2 value heads of a token
+    side by side) that lie apart, in place, and over one another."""
+    at = lambda head, token=0: FAKE + 2 * 128 * (12 * token + head)
+    packed = dict(qt=12 * 128, kt=12 * 128, qot=12 * 128, kot=12 * 128, q=at(0), k=at(8))
+    norm = lambda **c: call(S.LIB, "sz_qk_norm_rope", {**NORM, **packed}, **c)
+    for bad in (dict(qo=at(8), ko=at(8)), dict(qo=at(1), ko=at(8)), dict(qo=at(0), ko=at(7)), dict(qo=at(0), ko=at(9)),
+                dict(qo=at(0, 1), ko=at(8)), dict(qo=at(0) + 2, ko=at(8)), dict(qo=at(0), ko=at(0)),
+                dict(qo=at(4), ko=at(10)), dict(qo=at(0), qot=8 * 128, ko=at(8)), dict(qo=2 * FAKE, ko=2 * FAKE)):
+        assert norm(**bad) == S.SZ_ERR_INVALID_ARG, bad
+    read = lambda **c: call(S.LIB, "sz_cache_read", READ, **c)
+    assert read(k=FAKE, v=FAKE + 2 * 128) == S.SZ_ERR_INVALID_ARG
+    attend = lambda **c: call(S.LIB, "sz_cache_attend", ATTEND, **c)
+    for out in (FAKE, FAKE + 256, FAKE - 256, FAKE + 2048, FAKE + 2):
+        assert attend(out=out) == S.SZ_ERR_INVALID_ARG
+    # What lies apart gets as far as the workspace, which is too small here.
+    for change in (dict(out=FAKE + 4096), dict(qs=12 * 128, os=12 * 128, out=at(8), hq=4), dict(q=3 * FAKE)):
+        assert attend(**change, ws_bytes=0) in (S.SZ_ERR_CAPACITY, S.SZ_ERR_UNSUPPORTED, S.SZ_ERR_CUDA), change
