@@ -515,10 +515,11 @@ size_t sz_cache_evict_workspace_size(size_t batch, size_t kv_heads, size_t max_t
  *               < 2^31
  *  d_next_pos   int32 per sequence: the position its next token will have
  *  keep         1 .. 2^31 - 1
- *  d_new_lens   int32 per sequence: min(length, keep); not d_lens.  0 for a
- *               length outside [0, table_width * page_tokens], which is
- *               reported as SZ_ERR_INVALID_ARG, like a page id outside the
- *               pool (its tokens go first and are not moved)
+ *  d_new_lens   int32 per sequence: min(length, keep); refused where it shares
+ *               memory with d_lens or d_next_pos.  0 for a length outside
+ *               [0, table_width * page_tokens], which is reported as
+ *               SZ_ERR_INVALID_ARG, like a page id outside the pool (its
+ *               tokens go first and are not moved)
  *  d_ws         256-byte aligned workspace, contents irrelevant
  * batch is at most 65,535.  Asynchronous. */
 sz_status sz_cache_evict(void* d_pool, size_t pool_pages, size_t kv_heads, size_t head_dim, size_t page_tokens,

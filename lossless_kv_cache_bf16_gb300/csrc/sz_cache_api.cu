@@ -25,6 +25,11 @@ struct NvtxRange {
 };
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+// Whether `bytes` from a on and from b on share memory.
+bool ranges_overlap(const void* a, const void* b, uint64_t bytes) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return (x > y ? x - y : y - x) < bytes;
+}
 uint64_t align256(uint64_t x) { return (x + 255) & ~255ull; }
 
 sz_status from_cuda(cudaError_t e) {
@@ -315,8 +320,10 @@ sz_status sz_cache_evict(void* d_pool, size_t pool_pages, size_t kv_heads, size_
     if (!d_weight || !aligned(d_weight, 4) || !d_pos || !aligned(d_pos, 4)) return SZ_ERR_INVALID_ARG;
     if (!d_ws || !aligned(d_ws, 256) || (d_status && !aligned(d_status, 4))) return SZ_ERR_INVALID_ARG;
     if (batch > 0 && (!d_lens || !aligned(d_lens, 4) || !d_next_pos || !aligned(d_next_pos, 4) || !d_new_lens ||
-                      !aligned(d_new_lens, 4) || d_new_lens == d_lens))
+                      !aligned(d_new_lens, 4)))
         return SZ_ERR_INVALID_ARG;
+    // A list's blocks read the old lengths and positions while another's write the new lengths.
+    if (ranges_overlap(d_new_lens, d_lens, 4 * batch) || ranges_overlap(d_new_lens, d_next_pos, 4 * batch)) return SZ_ERR_INVALID_ARG;
     const uint64_t max_tokens = (uint64_t)table_width * page_tokens;
     if (ws_bytes < sz_cache_evict_workspace_size(batch, kv_heads, max_tokens)) return SZ_ERR_CAPACITY;
     const sz_status st = clear_status(d_status, stream);

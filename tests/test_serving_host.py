@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from tests.test_attend_host import ATTEND
-from tests.test_cache_host import FAKE, NORM, POOL, READ, Recorder, call
+from tests.test_cache_host import EVICT, FAKE, NORM, POOL, READ, Recorder, call
 
 
 @pytest.fixture(scope="module")
@@ -253,3 +253,13 @@ def test_rows_that_share_memory_with_an_output_are_refused(S):
     # What lies apart gets as far as the workspace, which is too small here.
     for change in (dict(out=FAKE + 4096), dict(qs=12 * 128, os=12 * 128, out=at(8), hq=4), dict(q=3 * FAKE)):
         assert attend(**change, ws_bytes=0) in (S.SZ_ERR_CAPACITY, S.SZ_ERR_UNSUPPORTED, S.SZ_ERR_CUDA), change
+
+
+def test_new_lengths_over_what_other_blocks_still_read_are_refused(S):
+    """Three sequences' lengths, each array shifted over another."""
+    evict = lambda **c: call(S.LIB, "sz_cache_evict", EVICT, batch=3, **c)
+    for off in (-8, -4, 0, 4, 8):
+        for change in (dict(nxt=3 * FAKE, new=FAKE + off), dict(nxt=3 * FAKE, new=3 * FAKE + off)):
+            assert evict(**change) == S.SZ_ERR_INVALID_ARG, change
+    for change in (dict(nxt=3 * FAKE, new=FAKE + 12), dict(nxt=3 * FAKE, new=3 * FAKE - 12), dict(nxt=FAKE, new=2 * FAKE)):
+        assert evict(**change, ws_bytes=0) == S.SZ_ERR_CAPACITY, change
