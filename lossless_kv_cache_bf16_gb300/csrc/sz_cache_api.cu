@@ -315,19 +315,20 @@ sz_status sz_cache_evict(void* d_pool, size_t pool_pages, size_t kv_heads, size_
     const NvtxRange range("sz_cache_evict");
     EvictParams p{};
     if (!pool_for(d_pool, pool_pages, kv_heads, head_dim, page_tokens, &p.pool)) return SZ_ERR_INVALID_ARG;
-    if (!table_ok(d_table, table_width, page_tokens) || batch > 65535) return SZ_ERR_INVALID_ARG;
+    if ((batch > 0 && !table_ok(d_table, table_width, page_tokens)) || batch > 65535) return SZ_ERR_INVALID_ARG;
     if (keep == 0 || keep >= (1ull << 31) || recent >= (1ull << 31)) return SZ_ERR_INVALID_ARG;
     if (!d_weight || !aligned(d_weight, 4) || !d_pos || !aligned(d_pos, 4)) return SZ_ERR_INVALID_ARG;
-    if (!d_ws || !aligned(d_ws, 256) || (d_status && !aligned(d_status, 4))) return SZ_ERR_INVALID_ARG;
-    if (batch > 0 && (!d_lens || !aligned(d_lens, 4) || !d_next_pos || !aligned(d_next_pos, 4) || !d_new_lens ||
-                      !aligned(d_new_lens, 4)))
+    if (d_status && !aligned(d_status, 4)) return SZ_ERR_INVALID_ARG;
+    if (batch == 0) return clear_status(d_status, stream);
+    if (!d_ws || !aligned(d_ws, 256)) return SZ_ERR_INVALID_ARG;
+    if (!d_lens || !aligned(d_lens, 4) || !d_next_pos || !aligned(d_next_pos, 4) || !d_new_lens || !aligned(d_new_lens, 4))
         return SZ_ERR_INVALID_ARG;
     // A list's blocks read the old lengths and positions while another's write the new lengths.
     if (ranges_overlap(d_new_lens, d_lens, 4 * batch) || ranges_overlap(d_new_lens, d_next_pos, 4 * batch)) return SZ_ERR_INVALID_ARG;
     const uint64_t max_tokens = (uint64_t)table_width * page_tokens;
     if (ws_bytes < sz_cache_evict_workspace_size(batch, kv_heads, max_tokens)) return SZ_ERR_CAPACITY;
     const sz_status st = clear_status(d_status, stream);
-    if (st != SZ_OK || batch == 0) return st;
+    if (st != SZ_OK) return st;
     p.table = d_table;
     p.table_width = (uint32_t)table_width;
     p.lens = d_lens;

@@ -263,3 +263,12 @@ def test_new_lengths_over_what_other_blocks_still_read_are_refused(S):
             assert evict(**change) == S.SZ_ERR_INVALID_ARG, change
     for change in (dict(nxt=3 * FAKE, new=FAKE + 12), dict(nxt=3 * FAKE, new=3 * FAKE - 12), dict(nxt=FAKE, new=2 * FAKE)):
         assert evict(**change, ws_bytes=0) == S.SZ_ERR_CAPACITY, change
+
+
+def test_an_empty_batch_has_nothing_to_evict(S):
+    """Tensors of no values have no address: none is asked for."""
+    none = dict(batch=0, table=None, lens=None, nxt=None, new=None)
+    assert call(S.LIB, "sz_cache_evict", EVICT, **none, ws=None, ws_bytes=0) == S.SZ_OK
+    assert call(S.LIB, "sz_cache_evict", EVICT, **none, width=0) == S.SZ_OK
+    for bad in (dict(pool=None), dict(weight=None), dict(keep=0), dict(status=FAKE + 2), dict(dim=96)):
+        assert call(S.LIB, "sz_cache_evict", EVICT, **none, **bad) == S.SZ_ERR_INVALID_ARG
