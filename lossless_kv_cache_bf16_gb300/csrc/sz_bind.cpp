@@ -127,7 +127,8 @@ PyObject* written_rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (PyErr_Occurred()) return nullptr;
     bool done[3] = {};
     long long reach = 0;
-    for (int turn = 0; turn < 3; turn++) {
+    const bool empty = size[0] == 0 || size[1] == 0 || size[2] == 0;
+    for (int turn = 0; turn < 3 && !empty; turn++) {
         int next = -1;
         for (int k = 0; k < 3; k++)
             if (!done[k] && (next < 0 || step[k] < step[next])) next = k;

@@ -480,6 +480,11 @@ def _table(table: torch.Tensor, batch: int, dev: int):
     return _pointer(table, _I32, -1, "table", dev), shape[1]
 
 
+def _same_places(shape, a, b) -> bool:
+    """Whether strides a and b put the values of that shape at the same places."""
+    return a == b or 0 in shape or all(n == 1 or x == y for n, x, y in zip(shape, a, b))
+
+
 def sz_cache_page_bytes(head_dim: int, kv_heads: int, page_tokens: int) -> int:
     return int(LIB.sz_cache_page_bytes(head_dim, kv_heads, page_tokens))
 
@@ -498,7 +503,7 @@ def sz_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor | N
         raise ValueError("q and k must have the same tokens and head dimension")
     qop, _, qos = _written_rows(q_out, _BF16, q_shape, "q_out", dev)
     kop, _, kos = _written_rows(k_out, _BF16, k_shape, "k_out", dev)
-    if (qp == qop and qs != qos) or (kp == kop and ks != kos):
+    if (qp == qop and not _same_places(q_shape, qs, qos)) or (kp == kop and not _same_places(k_shape, ks, kos)):
         raise ValueError("an output over its input must have the input's strides")
     _check("sz_qk_norm_rope", _bind.qk_norm_rope(
         _ADDRESS["sz_qk_norm_rope"], qp, qs[0], qs[1], q_heads, kp, ks[0], ks[1], k_shape[1], tokens, d,

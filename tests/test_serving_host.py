@@ -272,3 +272,35 @@ def test_an_empty_batch_has_nothing_to_evict(S):
     assert call(S.LIB, "sz_cache_evict", EVICT, **none, width=0) == S.SZ_OK
     for bad in (dict(pool=None), dict(weight=None), dict(keep=0), dict(status=FAKE + 2), dict(dim=96)):
         assert call(S.LIB, "sz_cache_evict", EVICT, **none, **bad) == S.SZ_ERR_INVALID_ARG
+
+
+def test_in_place_strides_that_no_row_uses_may_differ(S, monkeypatch):
+    """Norm and rotation in place: strides over one token, one head or none
+    place no row, and empty tensors all have the same address."""
+    rec = Recorder(S._bind)
+    monkeypatch.setattr(S, "_bind", rec)
+    view = lambda shape, strides: on_gpu(4096).as_strided(shape, strides)
+
+    def empty(shape, strides):
+        t = view(shape, strides)
+        t.data_ptr = lambda: 0
+        return t
+
+    q = on_gpu(3, 4, 64)
+
+    def norm(k, k_out, tokens=3, q=q, q_out=q):
+        S.sz_qk_norm_rope(q, k, None, None, 1e-6, on_gpu(32, dtype=torch.float32), on_gpu(tokens, dtype=torch.int32), q_out,
+                          k_out, stream=stream(-1))
+
+    norm(empty((3, 0, 64), (768, 64, 1)), empty((3, 0, 64), (0, 64, 1)))              # no key heads
+    norm(view((3, 1, 64), (768, 64, 1)), view((3, 1, 64), (768, 192, 1)))             # one key head
+    one = dict(tokens=1, q=view((1, 4, 64), (768, 64, 1)), q_out=view((1, 4, 64), (256, 64, 1)))
+    norm(view((1, 2, 64), (768, 64, 1)), view((1, 2, 64), (128, 64, 1)), **one)       # one token
+    none = dict(tokens=0, q=empty((0, 4, 64), (768, 64, 1)), q_out=empty((0, 4, 64), (256, 64, 1)))
+    norm(empty((0, 2, 64), (768, 64, 1)), empty((0, 2, 64), (128, 64, 1)), **none)
+    assert rec.calls == ["qk_norm_rope"] * 4
+    for k, k_out in ((view((3, 2, 64), (768, 64, 1)), view((3, 2, 64), (128, 64, 1))),
+                     (view((3, 2, 64), (768, 64, 1)), view((3, 2, 64), (768, 128, 1)))):
+        with pytest.raises(ValueError, match="strides"):
+            norm(k, k_out)
+    assert len(rec.calls) == 4
