@@ -115,6 +115,11 @@ class DecodeCache:
         if max(self.held) + 1 > self.capacity:
             raise ValueError("the cache is full")
         q, k, v = qkv[:, :hq], qkv[:, hq:hq + hk], qkv[:, hq + hk:]
+        shape = (self.batch, hq, self.head_dim)
+        if out is None:
+            out = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
+        else:  # before the token joins the cache: the attention's own refusal would come after it
+            S.check_output(out, shape, q)
         S.sz_qk_norm_rope(q, k, q_weight, k_weight, eps, inv_freq, self.next_pos, q, k)
         at = self.lens.long()
         slots = self.table.gather(1, (at // self.page)[:, None])[:, 0].long() * self.page + at % self.page
@@ -122,8 +127,6 @@ class DecodeCache:
         self.lens += 1
         self.next_pos += 1
         self.held = [n + 1 for n in self.held]
-        if out is None:
-            out = torch.empty((self.batch, hq, self.head_dim), dtype=torch.bfloat16, device=self.device)
         S.sz_cache_attend(q, self.pool, hk, self.page, self.table, self.lens, 1 / math.sqrt(self.head_dim), out,
                           self.attend_ws, weight=self.weight, status=self.status)
         if self.budget is not None and max(self.held) >= self.budget + self.page:

@@ -485,6 +485,14 @@ def _same_places(shape, a, b) -> bool:
     return a == b or 0 in shape or all(n == 1 or x == y for n, x, y in zip(shape, a, b))
 
 
+def check_output(out: torch.Tensor, shape, q: torch.Tensor) -> None:
+    """Raises where sz_cache_attend would refuse `out` as its output of that
+    shape for the queries q."""
+    device = q.get_device()
+    if _bind.overlap(_written_rows(out, _BF16, shape, "out", device), _rows(q, _BF16, "q", device)):
+        raise ValueError("out must not share memory with the queries")
+
+
 def sz_cache_page_bytes(head_dim: int, kv_heads: int, page_tokens: int) -> int:
     return int(LIB.sz_cache_page_bytes(head_dim, kv_heads, page_tokens))
 

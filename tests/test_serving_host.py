@@ -304,3 +304,25 @@ def test_in_place_strides_that_no_row_uses_may_differ(S, monkeypatch):
         with pytest.raises(ValueError, match="strides"):
             norm(k, k_out)
     assert len(rec.calls) == 4
+
+
+def test_a_step_with_a_bad_output_changes_nothing(cache):
+    state = lambda: (cache.lens.tolist(), cache.next_pos.tolist(), list(cache.held))
+    before, freq = state(), torch.ones(32)
+    qkv = on_gpu(2, 8, 64)
+
+    def at(t, address):
+        t.data_ptr = lambda: address
+        return t
+
+    far = 2 * FAKE
+    for out in (at(on_gpu(2, 4, 128), far), at(on_gpu(1, 4, 64), far), at(on_gpu(2, 256), far), bf16(2, 4, 64),
+                at(on_gpu(2, 4, 64, dtype=torch.float32), far), at(on_gpu(1, 4, 64).expand(2, 4, 64), far),
+                at(on_gpu(2, 4, 128)[:, :, ::2], far), at(on_gpu(2, 4, 64, gpu=1), far),
+                qkv[:, :4], at(qkv[:, 2:6], FAKE + 2 * 128)):
+        with pytest.raises(ValueError):
+            cache.step(qkv, None, None, freq, out=out)
+        assert cache.calls == [] and state() == before
+    for out in (at(on_gpu(2, 4, 64), far), at(qkv[:, 4:], FAKE + 4 * 128)):
+        assert cache.step(qkv, None, None, freq, out=out) is out
+    assert cache.held == [2, 2] and cache.calls == ["sz_qk_norm_rope", "sz_cache_append", "sz_cache_attend"] * 2
