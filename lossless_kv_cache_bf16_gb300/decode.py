@@ -45,6 +45,8 @@ class DecodeCache:
                  budget: int | None = None, recent: int = 0, device="cuda"):
         if budget is not None and not 0 < budget <= max_tokens - page_tokens:
             raise ValueError("the budget must leave a page of max_tokens")
+        if recent < 0:
+            raise ValueError("recent must not be negative")
         self.batch, self.q_heads, self.kv_heads, self.head_dim = batch, q_heads, kv_heads, head_dim
         self.page, self.budget, self.recent = page_tokens, budget, recent
         width = -(-max_tokens // page_tokens)
@@ -64,6 +66,9 @@ class DecodeCache:
         self.device = self.pool.device
         with self._gpu():
             need = S.sz_cache_attend_workspace_size(batch, q_heads, kv_heads, head_dim, self.capacity, True)
+        if need == 0:
+            raise ValueError(f"the attention takes up to 2,048 sequences and 1,024 query heads per kv head, not {batch} and "
+                             f"{q_heads} over {kv_heads}")
         self.attend_ws = new(need, torch.uint8)
         self.evict_ws = new(S.sz_cache_evict_workspace_size(batch, kv_heads, self.capacity), torch.uint8)
 

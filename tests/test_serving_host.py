@@ -326,3 +326,14 @@ def test_a_step_with_a_bad_output_changes_nothing(cache):
     for out in (at(on_gpu(2, 4, 64), far), at(qkv[:, 4:], FAKE + 4 * 128)):
         assert cache.step(qkv, None, None, freq, out=out) is out
     assert cache.held == [2, 2] and cache.calls == ["sz_qk_norm_rope", "sz_cache_append", "sz_cache_attend"] * 2
+
+
+def test_a_cache_whose_steps_would_be_refused_is_not_made(S):
+    from lossless_kv_cache_bf16_gb300 import decode
+
+    good = dict(batch=2, q_heads=8, kv_heads=4, head_dim=64, max_tokens=64, page_tokens=16, budget=16, recent=4, device="cpu")
+    decode.DecodeCache(**good)
+    for bad in (dict(q_heads=6), dict(q_heads=0), dict(q_heads=4 * 1025), dict(batch=2049), dict(head_dim=96), dict(kv_heads=0),
+                dict(page_tokens=24), dict(budget=0), dict(budget=49), dict(recent=-1)):
+        with pytest.raises(ValueError):
+            decode.DecodeCache(**{**good, **bad})
