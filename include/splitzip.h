@@ -365,8 +365,9 @@ sz_status sz_debug_encode_stalled(sz_dtype dt, const sz_codebook* h_cb, const vo
  * tokens of least accumulated attention weight.  The codec's pages have no
  * counterpart: the codec moves a KV cache without loss, this cache holds it
  * at 4.5 bits per value.  The conventions at the top of this file apply: the
- * caller owns every buffer, no call allocates, synchronises or keeps state,
- * and every call can be captured in a CUDA graph.  Values are bfloat16; sums,
+ * caller owns every buffer, which belongs to the current GPU like the stream,
+ * no call allocates, synchronises or keeps state, and every call can be
+ * captured in a CUDA graph.  Values are bfloat16; sums,
  * softmax statistics and norms are held in fp32.
  *
  * Strides are in elements; the head_dim channels of a row are contiguous.
@@ -412,11 +413,12 @@ size_t sz_cache_page_bytes(size_t head_dim, size_t kv_heads, size_t page_tokens)
  *  d_k_weight          without a norm
  *  rot_dim             a multiple of 16, 0 .. head_dim; the other channels are
  *                      normalised only
- *  d_inv_freq          rot_dim / 2 floats
+ *  d_inv_freq          rot_dim / 2 finite floats
  *  d_positions         one int32 per token
  *  d_q_out, d_k_out    may be the inputs (with the same strides); an output
  *                      that shares memory with other rows is refused
- * Asynchronous. */
+ * Range: the sum of a head's squares must stay below 2^128 (values below 2^59),
+ * else a normalised head comes out as zeros.  Asynchronous. */
 sz_status sz_qk_norm_rope(const void* d_q, int64_t q_token_stride, int64_t q_head_stride, size_t q_heads,
                           const void* d_k, int64_t k_token_stride, int64_t k_head_stride, size_t kv_heads,
                           size_t tokens, size_t head_dim, const void* d_q_weight, const void* d_k_weight, float eps,

@@ -35,7 +35,7 @@
 //
 // Measured: each 8 sequences of 32,768 tokens more (4 kv heads of 128, 28
 // query heads, 151 MB) take 26 us, 5.7 TB/s or 85% of the copy rate, after
-// 8 to 9 us that any call takes (launch, lengths, first copies, joins).  About
+// 13 us that any such call takes (launch, lengths, first copies, joins).  About
 // 650 instructions per 32 tokens and warp; 12 warps per SM with 168 registers
 // are faster than 16 with 128 (62 against 64 us for 16 such sequences), and
 // the scales' and codes' unpacking keeps the integer pipe half busy.
@@ -871,9 +871,9 @@ cudaError_t launch(const AttendParams& p, cudaStream_t s) {
     const uint64_t tokens = (uint64_t)p.table_width << p.pool.lg_page;
     // No more items than SMs, and a table with room for only 3 units a warp:
     // one item a block, and no join across blocks to launch.  With 8 items
-    // (32 heads over 8 of 128 channels) of 384 tokens 7.5 us against 10.4 in
-    // runs, of 768 tokens 8.9 against 10.4, of 1,152 (3 units a warp) 10.1
-    // against 10.1; of 1,536 11.8 against 10.5, but 12.0 against 15.2 with 128
+    // (32 heads over 8 of 128 channels) of 384 tokens 7.5 us against 10.2 in
+    // runs, of 768 tokens 8.9 against 10.5, of 1,152 (3 units a warp) 10.6
+    // against 10.2; of 1,536 11.8 against 10.5, but 12.3 against 15.5 with 128
     // items, so that far only where the items fill half the SMs.
     const uint64_t items = (uint64_t)p.batch * p.pool.heads * p.tiles;
     const uint64_t unit_a_warp = (uint64_t)Sh::kWarps * kUnitTokens;
@@ -892,7 +892,7 @@ cudaError_t launch(const AttendParams& p, cudaStream_t s) {
 template <int D>
 cudaError_t launch_dim(const AttendParams& p, cudaStream_t s) {
     // More than 8 query heads per kv head: items of 16, so that the cache is read
-    // once for all of them (12 heads, 16 sequences of 32,768 tokens: 89 us;
+    // once for all of them (12 heads, 16 sequences of 32,768 tokens: 88 us;
     // twice 61 us with items of 8).
     if (p.group <= 8) return p.weight ? launch<D, 1, true>(p, s) : launch<D, 1, false>(p, s);
     return p.weight ? launch<D, 2, true>(p, s) : launch<D, 2, false>(p, s);

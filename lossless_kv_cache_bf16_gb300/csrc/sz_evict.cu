@@ -508,13 +508,13 @@ cudaError_t launch_evict(const EvictParams& p, cudaStream_t s) {
     cudaError_t err = kernel_fit(reinterpret_cast<const void*>(evict_select_kernel<0>), kThreads, 0, &sms, &per_sm);
     if (err != cudaSuccess) return err;
     // As many blocks a list as fit on the device at once, while a thread has more
-    // than 8 keys (8,192 tokens, 8 heads: 9.8 us in one block, 12.3 in two, whose
-    // barriers cost more than the keys; 16,384: 25 us in one block with 16 of
-    // 32 keys, 13 in two or four), and at least as many as hold the longest
-    // sequence's keys, 32 a thread (beyond 8 blocks the keys are read again for
-    // every pass: 161 us for 524,288 tokens, 36 for 262,144).  16 keys have a
-    // kernel of their own: 32 spill, and 65,536 tokens in 32 lists take 23 us
-    // with it, 35 without.
+    // than 8 keys (8,192 tokens, 8 heads: 9.7 us in one block, 12.2 in two, whose
+    // barriers cost more than the keys; 16,384: 14.6 us in one block, 12.9 in
+    // two, 13.1 in four), and at least as many as hold the longest sequence's
+    // keys, 32 a thread (beyond 8 blocks the keys are read again for every pass:
+    // 4 heads of 524,288 tokens 160 us, 8 of 262,144 35).  16 keys have a kernel
+    // of their own: 32 spill, and 32 lists of 65,536 tokens take 19.4 us with
+    // it, 30.1 without; 8 of 16,384 in one block 14.6 and 24.8.
     const uint64_t lists = (uint64_t)p.pool.heads * p.batch, longest = (uint64_t)p.table_width << p.pool.lg_page;
     uint32_t cluster = 1;
     while (cluster < kMaxCluster && longest > 8ull * cluster * kThreads &&

@@ -5,8 +5,10 @@ it as a SplitZip stream, another decodes it bit for bit and generates tokens.
 ``DecodeCache`` is one layer's cache on that second machine: prompts come in
 as bf16 rows or straight from a stream, and every step normalises and rotates
 the new query and key, appends K and V, attends, and, with a budget, evicts
-the tokens of least accumulated attention weight.  All work runs in the
-library's kernels; this module keeps the lengths and calls them in order.
+the tokens of least accumulated attention weight.  The operators run in the
+library's kernels; this module keeps the lengths on the host and on the device,
+finds slots (with torch) and calls them in order.  The operators can be captured
+in CUDA graphs, a DecodeCache cannot: it decides on the host when to evict.
 
     python -m lossless_kv_cache_bf16_gb300.decode
 
@@ -38,8 +40,12 @@ def _on_its_gpu(method):
 class DecodeCache:
     """One layer's 4-bit cache of `batch` sequences of up to max_tokens tokens.
 
-    budget: tokens a sequence keeps when it has outgrown the budget by a page
-    (the `recent` last ones always among them); None keeps every token."""
+    budget: tokens a sequence keeps when it has outgrown the budget by a page;
+    None keeps every token.  The `recent` last ones are always among them as
+    long as recent <= budget, beyond that the budget goes to the weightiest of
+    them.  A prompt's tokens come with no weight: what a cut keeps of them goes
+    by the steps' queries alone.  A prompt must leave room for a token: a full
+    cache refuses steps."""
 
     def __init__(self, batch: int, q_heads: int, kv_heads: int, head_dim: int, max_tokens: int, page_tokens: int = 64,
                  budget: int | None = None, recent: int = 0, device="cuda"):
@@ -113,7 +119,8 @@ class DecodeCache:
     def step(self, qkv: torch.Tensor, q_weight, k_weight, inv_freq: torch.Tensor, eps: float = 1e-6,
              out: torch.Tensor | None = None) -> torch.Tensor:
         """One token of every sequence: qkv [batch, q heads + 2 kv heads, D] as
-        a layer's projection gives it; returns the attention [batch, q heads, D]."""
+        a layer's projection gives it, whose queries and keys are normalised and
+        rotated in place; returns the attention [batch, q heads, D]."""
         hq, hk = self.q_heads, self.kv_heads
         if qkv.shape != (self.batch, hq + 2 * hk, self.head_dim):
             raise ValueError(f"qkv must be {[self.batch, hq + 2 * hk, self.head_dim]}, not {list(qkv.shape)}")
