@@ -434,7 +434,9 @@ __global__ void __launch_bounds__(kThreads, MODE == kDraft ? 1 : 2) verify_kerne
                 for (uint32_t j = 0; j < n; j++) {
                     // A NaN or +infinity leaves a sum that is not 0.
                     best.runner += l[j] == kNegInf ? 0.f : l[j] * 0.f;
-                    if (l[j] > best.score) best.score = l[j], best.k = k + (int32_t)j;
+                    // Vectors come in ascending order, the single values in
+                    // front of them last.
+                    if (l[j] > best.score || (n == 1 && l[j] == best.score && k < best.k)) best.score = l[j], best.k = k + (int32_t)j;
                 }
             });
             const Draw got = join(best, [](Draw& x, const Draw& y) {
