@@ -471,14 +471,21 @@ __global__ void __launch_bounds__(Shape<D, N>::kThreads, 1) tree_kernel(const Tr
 #pragma unroll
                     for (int j = 0; j < NC; j += 16) tmem_load16(s_at + (n & 1u) * N + j, x + j);
                 };
-                for (uint32_t t = s.r0; t < s.r1; t++, n++) {
+                uint32_t t = s.r0;
+                // Of a group without rows the first warp alone follows the tiles: a
+                // warp that others do not wait for could fall two phases behind,
+                // and a parity does not tell two from none.
+                if (!used) {
+                    for (uint32_t k = n; warp % 4 == 0 && k < n + (s.r1 - t); k++) {
+                        attend_to(&bars.s_full[k & 1u], k >> 1 & 1u);
+                        if (lane == 0) mbar_arrive(&bars.p_full[k & 1u]);
+                    }
+                    n += s.r1 - t, t = s.r1;
+                }
+                for (; t < s.r1; t++, n++) {
                     const uint32_t buf = n & 1u;
                     attend_to(&bars.s_full[buf], n >> 1 & 1u);
                     tmem_fence_after();
-                    if (!used) {
-                        if (row == 0) mbar_arrive(&bars.p_full[buf]);
-                        continue;
-                    }
                     ask(n);
                     const float kf = s_kf[n & 3u][row];
                     const uint32_t token = t * kTile + row;
