@@ -671,8 +671,8 @@ __global__ void __launch_bounds__(Shape<D, N>::kThreads, 1) tree_kernel(const Tr
                         p.meta[4 * blockIdx.x] = (int32_t)s.b;
                     }
                 }
-                if (row < 4) s_nan[seg & 7u][g][row] = 0;
                 group_sync(bar_id);
+                if (row < 4) s_nan[seg & 7u][g][row] = 0;  // all have read it
             }
         }
     } else if (warp < Sh::kVWarp) {

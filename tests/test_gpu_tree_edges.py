@@ -33,3 +33,24 @@ def test_few_rows_among_many(lens, heads, group, nodes, counts, dim):
     c.check(*first)
     for _ in range(5):
         assert all(torch.equal(a, b) for a, b in zip(first, c.run()))
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("lens,heads,group,nodes", [([20000], 2, 4, 4), ([9000, 30000], 1, 4, 8), ([40000], 1, 7, 64),
+                                                    ([2500] * 20, 2, 4, 16)])
+def test_bad_nodes_behind_long_contexts(lens, heads, group, nodes, dim):
+    """Items whose last tokens are another block's than their first: a node whose
+    V is not finite reaches the nodes that attend to it, in its channels."""
+    c = tree.Case(lens, heads, group, dim, 32, nodes, seed=32)
+    rng, n = random.Random(dim + nodes), len(lens)
+    k, v = R.normal_bf16(R.gen(7), n, heads, dim), R.normal_bf16(R.gen(8), n, heads, dim)
+    want, slots = torch.zeros(n, nodes, heads * group, dim, dtype=torch.bool), []
+    for b in range(n):
+        node, head, channels = rng.randrange(nodes), rng.randrange(heads), rng.randrange(dim // 32)
+        v[b, head, 32 * channels + 5] = float("nan") if b % 2 else -float("inf")
+        slots.append(int(c.slots(b, lens[b] + nodes)[lens[b] + node]))
+        want[b, (c.mask[b] >> node & 1).bool(), head * group:(head + 1) * group, 32 * channels:32 * channels + 32] = True
+    c.write(k, v, torch.tensor(slots))
+    for _ in range(10):
+        out, lse = c.run()
+        assert torch.equal(torch.isnan(out).cpu(), want) and not bool(torch.isnan(lse).any())
