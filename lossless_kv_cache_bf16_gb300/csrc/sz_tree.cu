@@ -626,7 +626,12 @@ __global__ void __launch_bounds__(Shape<D, N>::kThreads, 1) tree_kernel(const Tr
                 tmem_wait_loads();
                 tmem_fence_before();
                 arrive(&bars.o_free);
-                if (!used) continue;
+                // V's warps mark for both groups.  What is left here would be another
+                // item's eight segments later.
+                if (!used) {
+                    if (row < 4) s_nan[seg & 7u][g][row] = 0;
+                    continue;
+                }
                 const uint32_t ch = channel_of<D>(row);
                 const uint64_t bad = row < D ? s_nan[seg & 7u][g][ch / 32] : 0ull;
                 if (bad) {

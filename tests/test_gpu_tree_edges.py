@@ -54,3 +54,29 @@ def test_bad_nodes_behind_long_contexts(lens, heads, group, nodes, dim):
     for _ in range(10):
         out, lse = c.run()
         assert torch.equal(torch.isnan(out).cpu(), want) and not bool(torch.isnan(lse).any())
+
+
+@pytest.mark.parametrize("group,counts", [(4, range(1, 17)), (8, range(1, 17)), (4, [16, 4, 4, 4]), (10, [16, 13, 0, 1])])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_bad_nodes_stay_in_their_sequence(dim, group, counts):
+    """Blocks with many items of one tile, some of few rows and some of many: a node
+    whose V is not finite reaches the nodes of its sequence that attend to it,
+    and no row of another one."""
+    rng, n, nodes = random.Random(dim + group), 1500, 16
+    counts = [rng.choice(list(counts)) for _ in range(n)]
+    c = tree.Case([rng.randrange(0, 100) for _ in range(n)], 1, group, dim, 16, nodes, seed=33, counts=counts)
+    bad = [b for b in range(n) if counts[b] and rng.random() < 0.4]
+    k, v = R.normal_bf16(R.gen(7), len(bad), 1, dim), R.normal_bf16(R.gen(8), len(bad), 1, dim)
+    want = torch.zeros(n, nodes, group, dim, dtype=torch.bool)
+    slots = []
+    for at, b in enumerate(bad):
+        # Roots most often, which every node attends to.
+        node, channels = 0 if rng.random() < 0.7 else rng.randrange(counts[b]), rng.randrange(dim // 32)
+        v[at, 0, 32 * channels + at % 32] = float("nan") if at % 2 else float("inf")
+        slots.append(int(c.slots(b, c.lens[b] + counts[b])[c.lens[b] + node]))
+        sees = (c.mask[b] >> node & 1).bool() & (torch.arange(nodes) < counts[b])
+        want[b, sees, :, 32 * channels:32 * channels + 32] = True
+    c.write(k, v, torch.tensor(slots))
+    for _ in range(3):
+        out, _ = c.run()
+        assert torch.equal(torch.isnan(out).cpu(), want)
