@@ -819,203 +819,204 @@ __global__ void __launch_bounds__(Shape<D, N>::kThreads, 1) tree_kernel(const Tr
             }
         };
         role();
-    } else if (warp == Sh::kLoad) {
-        // ======== raw tiles into the ring: lane 8 k + j has cell j of tile k of four ========
+    } else {
+        // One place for the warpgroup: its four warps have to come to the same instruction.
         fewer_registers<Sh::kOtherRegs>();
-        uint32_t n = 0;
-        auto role = [&]() {
-            Segment s;
-            for (Wk wk = walk; wk.next(s);) {
-                auto page_of = [&](uint32_t t) {
-                    const uint32_t tile = t + lane / 8, first = tile * kTile + lane % 8 * kCellTokens;
-                    return tile < s.r1 && first < s.tokens ? p.table[(uint64_t)s.b * p.table_width + (first >> lg_page)] : 0;
-                };
-                int32_t page = page_of(s.r0);
-                for (uint32_t t4 = s.r0; t4 < s.r1; t4 += 4) {
-                    const int32_t next_page = page_of(t4 + 4);
-                    const uint32_t tile = t4 + lane / 8, first = tile * kTile + lane % 8 * kCellTokens;
-                    uint32_t tokens = 0;
-                    const uint8_t* src = nullptr;
-                    if (tile < s.r1 && first < s.tokens) {
-                        if ((uint32_t)page < p.pool.pages) {
-                            tokens = min(s.tokens - first, kCellTokens);
-                            src = p.pool.base + cell_offset<D>(p.pool, (uint32_t)page, s.head, first & ((1u << lg_page) - 1u));
-                        } else if (p.status) {
-                            atomicMax(p.status, kStatusInvalid);
-                        }
-                    }
-                    const uint32_t held = __ballot_sync(0xFFFFFFFFu, tokens != 0);
-                    for (uint32_t k = 0; k < 4 && t4 + k < s.r1; k++, n++) {
-                        const uint32_t stage = n % RS;
-                        if (!wait(&bars.raw_free[stage], (n / RS & 1u) ^ 1u)) return;
-                        const bool my = lane / 8 == k;
-                        if (my) s_valid[stage][lane % 8] = (uint8_t)tokens;
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive_expect_tx(&bars.raw_full[stage], __popc(held >> (8 * k) & 0xFFu) * Sh::kCell);
-                        __syncwarp();
-                        if (my && tokens)
-                            bulk_g2s(smem + Sh::kRing + stage * Sh::kStageBytes + lane % 8 * Sh::kCell, src, Sh::kCell, &bars.raw_full[stage]);
-                    }
-                    page = next_page;
-                }
-            }
-        };
-        role();
-        // Copies still under way must land before the block gives its shared
-        // memory back.
-        for (uint32_t k = n > RS ? n - RS : 0; k < n; k++) mbar_wait(&bars.raw_full[k % RS], k / RS & 1u, p.wait_limit_ns);
-    } else if (warp == Sh::kMma) {
-        // ======== matrix instructions: one thread waits and issues ========
-        fewer_registers<Sh::kOtherRegs>();
-        if (one_lane()) {
+        if (warp == Sh::kLoad) {
+            // ======== raw tiles into the ring: lane 8 k + j has cell j of tile k of four ========
+            uint32_t n = 0;
             auto role = [&]() {
-                uint32_t n = 0, seg = 0;
-                bool pending = false, first = false, last = false;  // O of the tile before
-                uint32_t p_seg = 0, p_shape = 0;
-                auto product = [&](uint32_t m) {
-                    const uint32_t buf = m & 1u, v = m % Sh::kV;
-                    if (!wait_alone(&bars.v_full[v], m / Sh::kV & 1u) || !wait_alone(&bars.p_full[buf], m >> 1 & 1u)) return false;
-                    if (first && !wait_alone(&bars.o_free, (p_seg & 1u) ^ 1u)) return false;
-                    tmem_fence_after();
-                    const uint32_t a = tmem + Sh::kVCol + v * 64, d = tmem + Sh::kOCol;
-                    const SmemOperand w(smem_u32(smem + Sh::kP) + buf * Sh::kPBytes, 128, kTile * 16);
-                    if (first)
-                        mma_tmem_smem<false>(d, a, w, 0, p_shape);
-                    else
-                        mma_tmem_smem<true>(d, a, w, 0, p_shape);
-#pragma unroll
-                    for (int k = 1; k < 8; k++) mma_tmem_smem<true>(d, a + 8 * k, w, 256 * k, p_shape);
-                    mma_commit(&bars.pv[v]);
-                    if (last) {
-                        mma_commit(&bars.o_full);
-                        mbar_arrive(&bars.o_full);
-                    }
-                    return true;
-                };
                 Segment s;
-                for (Wk wk = walk; wk.next(s); seg++) {
-                    const uint32_t cols = (s.rows + Sh::kCols - 1) / Sh::kCols * Sh::kCols;  // of whole groups
-                    const uint32_t shape = mma_shape(false, false, cols);
-                    if (!wait_alone(&bars.q_full[seg & 1u], seg >> 1 & 1u)) return;
-                    const SmemOperand q_op(smem_u32(smem) + (seg & 1u) * Sh::kQBytes, N * 16, 128);
-                    for (uint32_t t = s.r0; t < s.r1; t++, n++) {
-                        const uint32_t buf = n & 1u;
-                        // S of tile n - 2 has been read: O of that tile, issued
-                        // before this, has waited for its weights.
-                        if (!wait_alone(&bars.k_full[buf], n >> 1 & 1u)) return;
-                        tmem_fence_after();
-                        const uint32_t d = tmem + Sh::kSCol + buf * N, a = tmem + Sh::kKCol + buf * (D / 2);
-                        mma_tmem_smem<false>(d, a, q_op, 0, shape);
-#pragma unroll
-                        for (int k = 1; k < D / 16; k++) mma_tmem_smem<true>(d, a + 8 * k, q_op, 2 * k * (N * 16), shape);
-                        mma_commit(&bars.s_full[buf]);
-                        mbar_arrive(&bars.s_full[buf]);
-                        if (t + 1 == s.r1) mma_commit(&bars.q_free[seg & 1u]);
-                        if (pending && !product(n - 1)) return;
-                        pending = true;
-                        first = t == s.r0, last = t + 1 == s.r1;
-                        p_seg = seg, p_shape = mma_shape(true, true, cols);
+                for (Wk wk = walk; wk.next(s);) {
+                    auto page_of = [&](uint32_t t) {
+                        const uint32_t tile = t + lane / 8, first = tile * kTile + lane % 8 * kCellTokens;
+                        return tile < s.r1 && first < s.tokens ? p.table[(uint64_t)s.b * p.table_width + (first >> lg_page)] : 0;
+                    };
+                    int32_t page = page_of(s.r0);
+                    for (uint32_t t4 = s.r0; t4 < s.r1; t4 += 4) {
+                        const int32_t next_page = page_of(t4 + 4);
+                        const uint32_t tile = t4 + lane / 8, first = tile * kTile + lane % 8 * kCellTokens;
+                        uint32_t tokens = 0;
+                        const uint8_t* src = nullptr;
+                        if (tile < s.r1 && first < s.tokens) {
+                            if ((uint32_t)page < p.pool.pages) {
+                                tokens = min(s.tokens - first, kCellTokens);
+                                src = p.pool.base + cell_offset<D>(p.pool, (uint32_t)page, s.head, first & ((1u << lg_page) - 1u));
+                            } else if (p.status) {
+                                atomicMax(p.status, kStatusInvalid);
+                            }
+                        }
+                        const uint32_t held = __ballot_sync(0xFFFFFFFFu, tokens != 0);
+                        for (uint32_t k = 0; k < 4 && t4 + k < s.r1; k++, n++) {
+                            const uint32_t stage = n % RS;
+                            if (!wait(&bars.raw_free[stage], (n / RS & 1u) ^ 1u)) return;
+                            const bool my = lane / 8 == k;
+                            if (my) s_valid[stage][lane % 8] = (uint8_t)tokens;
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive_expect_tx(&bars.raw_full[stage], __popc(held >> (8 * k) & 0xFFu) * Sh::kCell);
+                            __syncwarp();
+                            if (my && tokens)
+                                bulk_g2s(smem + Sh::kRing + stage * Sh::kStageBytes + lane % 8 * Sh::kCell, src, Sh::kCell, &bars.raw_full[stage]);
+                        }
+                        page = next_page;
                     }
                 }
-                if (pending) product(n - 1);
             };
             role();
-            // Nothing is under way when tensor memory is given back.
-            mma_commit(&bars.end);
-            mbar_wait(&bars.end, 0, p.wait_limit_ns);
-        }
-        __syncwarp();
-    } else {
-        // ======== queries: rows as they are into shared memory, then a lane a row,
-        // or where there are fewer than 64 rows, kParts lanes of both warps ========
-        fewer_registers<Sh::kOtherRegs>();
-        const uint32_t wq = warp - Sh::kQuery, c = N == 64 ? 32 * wq + lane : lane % N;
-        const uint32_t part = N == 64 ? 0u : N == 32 ? wq : 2 * wq + lane / 16;
-        uint32_t seg = 0;
-        bool asked = false;
-        auto role = [&]() {
-            Segment s;
-            uint8_t* raw = smem + Sh::kRows + c * Sh::kRow;
-            for (Wk wk = walk; wk.next(s); seg++) {
-                if (!wait(&bars.q_free[seg & 1u], (seg >> 1 & 1u) ^ 1u)) return;
-                // Both warps have read the rows of the segment before.
-                if (Sh::kParts > 1 && seg && !wait(&bars.q_full[(seg - 1) & 1u], (seg - 1) >> 1 & 1u)) return;
-                const bool there = c < s.rows;
-                const uint32_t r = s.row0 + c, node = there ? r / p.group : 0u;
-                const uint16_t* src = p.q + (int64_t)s.b * p.q_seq + (int64_t)node * p.q_node + (int64_t)(s.head * p.group + r - node * p.group) * p.q_head;
-                if (p.q_vec) {
-                    const bool mine = there && (N == 64 || (lane < N && lane % 2 == wq));
-                    const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, mine)) * (2 * D);
-                    if (lane == 0) mbar_arrive_expect_tx(&bars.q_raw[wq], bytes);
-                    __syncwarp();
-                    asked = true;
-                    if (mine) bulk_g2s(raw, src, 2 * D, &bars.q_raw[wq]);
-                } else if (there) {
-#pragma unroll 1
-                    for (uint32_t k = 0; k < D; k++) reinterpret_cast<uint16_t*>(raw)[k] = src[k];
-                }
-                const bool sees = N == 64 || wq == 1;  // this warp's to find out
-                const uint64_t mask = there && sees ? p.mask[(uint64_t)s.b * p.nodes + node] : 0ull;
-                // Rows' bits of nodes into nodes' bits of rows, lane k the node k.
-#pragma unroll 1
-                for (uint32_t k0 = 0; sees && k0 < s.tokens - s.len; k0 += 32) {
-                    const uint32_t bits = (uint32_t)(mask >> k0);
-                    uint32_t mine = 0;
-#pragma unroll 8
-                    for (uint32_t k = 0; k < 32; k++) {
-                        const uint32_t seen = __ballot_sync(0xFFFFFFFFu, bits >> k & 1u);
-                        mine = lane == k ? seen : mine;
-                    }
-                    s_seen[seg & 7u][N == 64 ? wq : 0u][k0 + lane] = mine;
-                }
-                if (p.q_vec && (!wait(&bars.q_raw[wq], seg & 1u) || (Sh::kParts > 1 && !wait(&bars.q_raw[wq ^ 1u], seg & 1u)))) return;
-                asked = false;
-                {
-                    constexpr uint32_t kHalves = N == 16 ? 2 : 1;
-                    uint32_t top = 0;
-#pragma unroll 4
-                    for (uint32_t k = 0; k < D / 8 / kHalves; k++) {
-                        if (!there) continue;
-                        const uint4 v = *reinterpret_cast<const uint4*>(raw + 16 * (k + (kHalves == 2 ? lane / 16 * (D / 16) : 0u)));
-                        const uint32_t m = max_u16x2(max_u16x2(v.x & 0x7F807F80u, v.y & 0x7F807F80u), max_u16x2(v.z & 0x7F807F80u, v.w & 0x7F807F80u));
-                        top = max(top, max(m & 0xFFFFu, m >> 16));
-                    }
-                    if (kHalves == 2) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16));
-                    const bool fine = top != 0x7F80u;
-                    int up = max((int)(top >> 7) - 127, kMinExp);
-                    const int most = (int)__reduce_max_sync(0xFFFFFFFFu, (uint32_t)(top && fine ? up + 128 : 0)) - 128;
-                    const int least = (int)__reduce_min_sync(0xFFFFFFFFu, (uint32_t)(top && fine ? up + 128 : 1000)) - 128;
-                    // Rows that are not finite have a factor of their own.
-                    const bool common = __all_sync(0xFFFFFFFFu, fine) && most - least <= kShareExp;
-                    if (common) up = max(most, kMinExp);
-                    const float unit = copysignf(pow2(14 - up), p.scale_log2);
-                    uint8_t* dst = smem + (seg & 1u) * Sh::kQBytes + c * 16;
-#pragma unroll 2
-                    for (uint32_t k = part * (D / 8 / Sh::kParts); k < (part + 1) * (D / 8 / Sh::kParts); k++) {
-                        const uint4 u = *reinterpret_cast<const uint4*>(raw + 16 * k);
-                        const uint32_t v[4] = {u.x, u.y, u.z, u.w};
-                        float f[8];
-#pragma unroll
-                        for (int j = 0; j < 4; j++) {
-                            f[2 * j] = there && fine ? __uint_as_float(v[j] << 16) * unit : 0.f;
-                            f[2 * j + 1] = there && fine ? __uint_as_float(v[j] & 0xFFFF0000u) * unit : 0.f;
+            // Copies still under way must land before the block gives its shared
+            // memory back.
+            for (uint32_t k = n > RS ? n - RS : 0; k < n; k++) mbar_wait(&bars.raw_full[k % RS], k / RS & 1u, p.wait_limit_ns);
+        } else if (warp == Sh::kMma) {
+            // ======== matrix instructions: one thread waits and issues ========
+            if (one_lane()) {
+                auto role = [&]() {
+                    uint32_t n = 0, seg = 0;
+                    bool pending = false, first = false, last = false;  // O of the tile before
+                    uint32_t p_seg = 0, p_shape = 0;
+                    auto product = [&](uint32_t m) {
+                        const uint32_t buf = m & 1u, v = m % Sh::kV;
+                        if (!wait_alone(&bars.v_full[v], m / Sh::kV & 1u) || !wait_alone(&bars.p_full[buf], m >> 1 & 1u)) return false;
+                        if (first && !wait_alone(&bars.o_free, (p_seg & 1u) ^ 1u)) return false;
+                        tmem_fence_after();
+                        const uint32_t a = tmem + Sh::kVCol + v * 64, d = tmem + Sh::kOCol;
+                        const SmemOperand w(smem_u32(smem + Sh::kP) + buf * Sh::kPBytes, 128, kTile * 16);
+                        if (first)
+                            mma_tmem_smem<false>(d, a, w, 0, p_shape);
+                        else
+                            mma_tmem_smem<true>(d, a, w, 0, p_shape);
+    #pragma unroll
+                        for (int k = 1; k < 8; k++) mma_tmem_smem<true>(d, a + 8 * k, w, 256 * k, p_shape);
+                        mma_commit(&bars.pv[v]);
+                        if (last) {
+                            mma_commit(&bars.o_full);
+                            mbar_arrive(&bars.o_full);
                         }
-                        // Channels 32 i + 8 q + 4 h + e are k 32 i + 16 (e / 2) + 4 q + 2 (e % 2) + h.
-                        uint8_t* to = dst + (4 * (k / 4) + k % 4 / 2) * (N * 16) + k % 2 * 8;
-                        *reinterpret_cast<uint2*>(to) = make_uint2(pack_f16(f[0], f[4]), pack_f16(f[1], f[5]));
-                        *reinterpret_cast<uint2*>(to + 2 * (N * 16)) = make_uint2(pack_f16(f[2], f[6]), pack_f16(f[3], f[7]));
+                        return true;
+                    };
+                    Segment s;
+                    for (Wk wk = walk; wk.next(s); seg++) {
+                        const uint32_t cols = (s.rows + Sh::kCols - 1) / Sh::kCols * Sh::kCols;  // of whole groups
+                        const uint32_t shape = mma_shape(false, false, cols);
+                        if (!wait_alone(&bars.q_full[seg & 1u], seg >> 1 & 1u)) return;
+                        const SmemOperand q_op(smem_u32(smem) + (seg & 1u) * Sh::kQBytes, N * 16, 128);
+                        for (uint32_t t = s.r0; t < s.r1; t++, n++) {
+                            const uint32_t buf = n & 1u;
+                            // S of tile n - 2 has been read: O of that tile, issued
+                            // before this, has waited for its weights.
+                            if (!wait_alone(&bars.k_full[buf], n >> 1 & 1u)) return;
+                            tmem_fence_after();
+                            const uint32_t d = tmem + Sh::kSCol + buf * N, a = tmem + Sh::kKCol + buf * (D / 2);
+                            mma_tmem_smem<false>(d, a, q_op, 0, shape);
+    #pragma unroll
+                            for (int k = 1; k < D / 16; k++) mma_tmem_smem<true>(d, a + 8 * k, q_op, 2 * k * (N * 16), shape);
+                            mma_commit(&bars.s_full[buf]);
+                            mbar_arrive(&bars.s_full[buf]);
+                            if (t + 1 == s.r1) mma_commit(&bars.q_free[seg & 1u]);
+                            if (pending && !product(n - 1)) return;
+                            pending = true;
+                            first = t == s.r0, last = t + 1 == s.r1;
+                            p_seg = seg, p_shape = mma_shape(true, true, cols);
+                        }
                     }
-                    const float rf = ldexpf(fabsf(p.scale_log2), up - 4);
-                    if (part == 0) s_rf[seg & 3u][c] = !there ? 0.f : fine ? rf : __int_as_float(0x7FC00000);
-                    if (lane == 0 && (N == 64 || wq == 0)) s_common[seg & 3u][N == 64 ? wq : 0u] = common ? rf : -1.f;
-                }
-                fence_async_smem();
-                arrive(&bars.q_full[seg & 1u]);
+                    if (pending) product(n - 1);
+                };
+                role();
+                // Nothing is under way when tensor memory is given back.
+                mma_commit(&bars.end);
+                mbar_wait(&bars.end, 0, p.wait_limit_ns);
             }
-        };
-        if (wq < Sh::kQueries) role();
-        // As with the ring.
-        if (asked) mbar_wait(&bars.q_raw[wq], seg & 1u, p.wait_limit_ns);
+            __syncwarp();
+        } else {
+            // ======== queries: rows as they are into shared memory, then a lane a row,
+            // or where there are fewer than 64 rows, kParts lanes of both warps ========
+            const uint32_t wq = warp - Sh::kQuery, c = N == 64 ? 32 * wq + lane : lane % N;
+            const uint32_t part = N == 64 ? 0u : N == 32 ? wq : 2 * wq + lane / 16;
+            uint32_t seg = 0;
+            bool asked = false;
+            auto role = [&]() {
+                Segment s;
+                uint8_t* raw = smem + Sh::kRows + c * Sh::kRow;
+                for (Wk wk = walk; wk.next(s); seg++) {
+                    if (!wait(&bars.q_free[seg & 1u], (seg >> 1 & 1u) ^ 1u)) return;
+                    // Both warps have read the rows of the segment before.
+                    if (Sh::kParts > 1 && seg && !wait(&bars.q_full[(seg - 1) & 1u], (seg - 1) >> 1 & 1u)) return;
+                    const bool there = c < s.rows;
+                    const uint32_t r = s.row0 + c, node = there ? r / p.group : 0u;
+                    const uint16_t* src = p.q + (int64_t)s.b * p.q_seq + (int64_t)node * p.q_node + (int64_t)(s.head * p.group + r - node * p.group) * p.q_head;
+                    if (p.q_vec) {
+                        const bool mine = there && (N == 64 || (lane < N && lane % 2 == wq));
+                        const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, mine)) * (2 * D);
+                        if (lane == 0) mbar_arrive_expect_tx(&bars.q_raw[wq], bytes);
+                        __syncwarp();
+                        asked = true;
+                        if (mine) bulk_g2s(raw, src, 2 * D, &bars.q_raw[wq]);
+                    } else if (there) {
+    #pragma unroll 1
+                        for (uint32_t k = 0; k < D; k++) reinterpret_cast<uint16_t*>(raw)[k] = src[k];
+                    }
+                    const bool sees = N == 64 || wq == 1;  // this warp's to find out
+                    const uint64_t mask = there && sees ? p.mask[(uint64_t)s.b * p.nodes + node] : 0ull;
+                    // Rows' bits of nodes into nodes' bits of rows, lane k the node k.
+    #pragma unroll 1
+                    for (uint32_t k0 = 0; sees && k0 < s.tokens - s.len; k0 += 32) {
+                        const uint32_t bits = (uint32_t)(mask >> k0);
+                        uint32_t mine = 0;
+    #pragma unroll 8
+                        for (uint32_t k = 0; k < 32; k++) {
+                            const uint32_t seen = __ballot_sync(0xFFFFFFFFu, bits >> k & 1u);
+                            mine = lane == k ? seen : mine;
+                        }
+                        s_seen[seg & 7u][N == 64 ? wq : 0u][k0 + lane] = mine;
+                    }
+                    if (p.q_vec && (!wait(&bars.q_raw[wq], seg & 1u) || (Sh::kParts > 1 && !wait(&bars.q_raw[wq ^ 1u], seg & 1u)))) return;
+                    asked = false;
+                    {
+                        constexpr uint32_t kHalves = N == 16 ? 2 : 1;
+                        uint32_t top = 0;
+    #pragma unroll 4
+                        for (uint32_t k = 0; k < D / 8 / kHalves; k++) {
+                            if (!there) continue;
+                            const uint4 v = *reinterpret_cast<const uint4*>(raw + 16 * (k + (kHalves == 2 ? lane / 16 * (D / 16) : 0u)));
+                            const uint32_t m = max_u16x2(max_u16x2(v.x & 0x7F807F80u, v.y & 0x7F807F80u), max_u16x2(v.z & 0x7F807F80u, v.w & 0x7F807F80u));
+                            top = max(top, max(m & 0xFFFFu, m >> 16));
+                        }
+                        if (kHalves == 2) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16));
+                        const bool fine = top != 0x7F80u;
+                        int up = max((int)(top >> 7) - 127, kMinExp);
+                        const int most = (int)__reduce_max_sync(0xFFFFFFFFu, (uint32_t)(top && fine ? up + 128 : 0)) - 128;
+                        const int least = (int)__reduce_min_sync(0xFFFFFFFFu, (uint32_t)(top && fine ? up + 128 : 1000)) - 128;
+                        // Rows that are not finite have a factor of their own.
+                        const bool common = __all_sync(0xFFFFFFFFu, fine) && most - least <= kShareExp;
+                        if (common) up = max(most, kMinExp);
+                        const float unit = copysignf(pow2(14 - up), p.scale_log2);
+                        uint8_t* dst = smem + (seg & 1u) * Sh::kQBytes + c * 16;
+    #pragma unroll 2
+                        for (uint32_t k = part * (D / 8 / Sh::kParts); k < (part + 1) * (D / 8 / Sh::kParts); k++) {
+                            const uint4 u = *reinterpret_cast<const uint4*>(raw + 16 * k);
+                            const uint32_t v[4] = {u.x, u.y, u.z, u.w};
+                            float f[8];
+    #pragma unroll
+                            for (int j = 0; j < 4; j++) {
+                                f[2 * j] = there && fine ? __uint_as_float(v[j] << 16) * unit : 0.f;
+                                f[2 * j + 1] = there && fine ? __uint_as_float(v[j] & 0xFFFF0000u) * unit : 0.f;
+                            }
+                            // Channels 32 i + 8 q + 4 h + e are k 32 i + 16 (e / 2) + 4 q + 2 (e % 2) + h.
+                            uint8_t* to = dst + (4 * (k / 4) + k % 4 / 2) * (N * 16) + k % 2 * 8;
+                            *reinterpret_cast<uint2*>(to) = make_uint2(pack_f16(f[0], f[4]), pack_f16(f[1], f[5]));
+                            *reinterpret_cast<uint2*>(to + 2 * (N * 16)) = make_uint2(pack_f16(f[2], f[6]), pack_f16(f[3], f[7]));
+                        }
+                        const float rf = ldexpf(fabsf(p.scale_log2), up - 4);
+                        if (part == 0) s_rf[seg & 3u][c] = !there ? 0.f : fine ? rf : __int_as_float(0x7FC00000);
+                        if (lane == 0 && (N == 64 || wq == 0)) s_common[seg & 3u][N == 64 ? wq : 0u] = common ? rf : -1.f;
+                    }
+                    fence_async_smem();
+                    arrive(&bars.q_full[seg & 1u]);
+                }
+            };
+            if (wq < Sh::kQueries) role();
+            // As with the ring.
+            if (asked) mbar_wait(&bars.q_raw[wq], seg & 1u, p.wait_limit_ns);
+        }
     }
     tmem_fence_before();
     __syncthreads();
