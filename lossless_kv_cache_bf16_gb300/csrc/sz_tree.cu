@@ -364,10 +364,12 @@ __global__ void __launch_bounds__(Shape<D, N>::kThreads, 1) tree_kernel(const Tr
     for (uint32_t b = blockIdx.x; b < p.batch; b += gridDim.x) {
         const uint32_t c = s_cnt[b];
         if (!(c & 0x80u)) continue;
-        for (uint32_t x = tid; x < (c & 0x7Fu) * q_heads * D; x += Sh::kThreads) {
-            const uint32_t node = x / (q_heads * D), h = x / D % q_heads;
-            p.out[(int64_t)b * p.out_seq + (int64_t)node * p.out_node + (int64_t)h * p.out_head + x % D] = 0;
-            if (p.lse && x % D == 0) p.lse[((uint64_t)b * p.nodes + node) * q_heads + h] = kNegInf;
+        // A warp a row: there may be 2^28 of them, and 2^35 channels.
+        for (uint32_t r = warp; r < (c & 0x7Fu) * q_heads; r += Sh::kThreads / 32) {
+            const uint32_t node = r / q_heads, h = r % q_heads;
+            uint16_t* out = p.out + (int64_t)b * p.out_seq + (int64_t)node * p.out_node + (int64_t)h * p.out_head;
+            for (uint32_t k = lane; k < D; k += 32) out[k] = 0;
+            if (p.lse && lane == 0) p.lse[((uint64_t)b * p.nodes + node) * q_heads + h] = kNegInf;
         }
     }
     if (tid == 0) p.meta[4 * blockIdx.x] = -1;

@@ -80,3 +80,19 @@ def test_bad_nodes_stay_in_their_sequence(dim, group, counts):
     for _ in range(3):
         out, _ = c.run()
         assert torch.equal(torch.isnan(out).cpu(), want)
+
+
+def test_rows_of_a_wide_sequence_that_cannot_be_served():
+    """2^32 outputs of a sequence with a negative length: all zero."""
+    S, nodes, heads, group, dim = tree.S, 64, 512, 1024, 128
+    hq = heads * group
+    pool = torch.zeros(1, R.page_bytes(dim, heads, 16), dtype=torch.uint8, device="cuda")
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    out = torch.full((1, nodes, hq, dim), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse, status = torch.full((1, nodes, hq), 7.0, device="cuda"), i32([-1])
+    ws = torch.empty(S.sz_cache_attend_tree_workspace_size(1, nodes, hq, heads, dim, 16), dtype=torch.uint8, device="cuda")
+    q = torch.zeros(1, 1, 1, dim, dtype=torch.bfloat16, device="cuda").expand(1, nodes, hq, dim)
+    S.sz_cache_attend_tree(q, pool, heads, 16, i32([[0]]), i32([-1]), torch.ones(1, nodes, dtype=torch.int64, device="cuda"), 0.1, out, ws,
+                           lse=lse, status=status)
+    assert status.item() == S.SZ_ERR_INVALID_ARG
+    assert all(bool((out[0, j] == 0).all()) for j in range(nodes)) and bool((lse == -float("inf")).all())
