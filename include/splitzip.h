@@ -624,7 +624,7 @@ size_t sz_verify_tree_workspace_size(size_t batch, size_t nodes, size_t vocab);
  *  d_counts     nullable: int32 nodes of each sequence, 0 .. nodes (others
  *               count as 0 and are reported): without any, accepted is 0 and
  *               the next token -1
- *  scale        above 0: the inverse temperature
+ *  scale        above 0 and at most 2^127: the inverse temperature
  *  d_uniforms   float [batch][nodes] in [0, 1)
  *  d_noise      float [batch][vocab] by noise_stride, above 0; an entry that is
  *               not, or is infinite, takes its token out of the draw

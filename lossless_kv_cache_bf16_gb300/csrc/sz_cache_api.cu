@@ -494,7 +494,7 @@ sz_status sz_verify_tree(const void* d_logits, int logits_f32, int64_t seq_strid
     const NvtxRange range("sz_verify_tree");
     VerifyParams p{};
     const int size = logits_f32 ? 4 : 2;
-    if (!verify_sizes_ok(batch, nodes, vocab) || !std::isfinite(scale) || !(scale > 0.f)) return SZ_ERR_INVALID_ARG;
+    if (!verify_sizes_ok(batch, nodes, vocab) || !(scale > 0.f && scale <= 0x1p127f)) return SZ_ERR_INVALID_ARG;
     if (d_status && !aligned(d_status, 4)) return SZ_ERR_INVALID_ARG;
     if (batch == 0) return clear_status(d_status, stream);
     if (!d_logits || !aligned(d_logits, size)) return SZ_ERR_INVALID_ARG;

@@ -173,14 +173,16 @@ struct Residual {
     const float* noise;
     float c;              // scale * log2(e)
     float scale;
-    float mp, mq, a, b;   // a 2^(c (l - mp)) - b 2^(c (d - mq))
+    float mp, mq, a, b;   // a 2^(c (l - mp)) - b 2^(c (d - mq)); mp the row's largest logit
     template <bool DRAFT>
     __device__ __forceinline__ float score(float l, float d, float e) const {
         if constexpr (DRAFT) {
             const float r = a * exp2_fast((l - mp) * c) - b * exp2_fast((d - mq) * c);
             return r > 0.f ? log2_fast(r) - log2_fast(e) : kNegInf;
         } else {
-            return fmaf(l, c, -log2_fast(e));
+            // Less the row's largest logit, so that neither overflows nor takes
+            // the noise's bits.
+            return fmaf(l - mp, c, -log2_fast(e));
         }
     }
     // ln(r / e) in fp64.
@@ -192,11 +194,11 @@ struct Residual {
                              (double)b * exp(((double)value_at(q, k) - (double)mq) * (double)scale);
             return log(r) - log(e);
         } else {
-            return l * (double)scale - log(e);
+            return (l - (double)mp) * (double)scale - log(e);
         }
     }
-    // Whether the winner of a draw is sure: lg2 and the fma are good to 2^-22 of
-    // operands below 200.
+    // Whether the winner of a draw is sure: lg2 is good to 2^-22 of numbers below
+    // 150, the difference and the fma to 2^-24 of numbers below 150 + |s|.
     static __device__ __forceinline__ float doubt(float s) { return 1e-4f + 1e-6f * fabsf(s); }
 };
 
@@ -514,6 +516,7 @@ __global__ void __launch_bounds__(kThreads, MODE == kDraft ? 1 : 2) verify_kerne
             const uint32_t first = s_first[0] ? __ffs(s_first[0]) - 1 : s_first[1] ? 31 + __ffs(s_first[1]) : children;
             if (first < children) go = s_child[first];
             next = -1;
+            res.mp = m;
             if (go < 0 && fine) {
                 Draw best{kNegInf, -1, kNegInf};
                 sweep(row, row, noise, no, yes, [&](int32_t k, const auto& l, const auto&, const auto& e) {
@@ -565,8 +568,9 @@ __global__ void __launch_bounds__(kThreads, MODE == kDraft ? 1 : 2) verify_kerne
                 if ((uint32_t)t < p.vocab) {
                     // u q < r over q, from the logits' difference: neither
                     // underflows, and a q of 0 leaves an infinity where p is above 0.
-                    const float x = (s_w[j] - sp.m) * c, y = (s_q[j] - sq.m) * c;
-                    if (s_uniform[s_child[j]] + bq < res.a * sq.sum * exp2_fast(x - y)) {
+                    // Their products with c may overflow one by one.
+                    const float x = (s_w[j] - sp.m) - (s_q[j] - sq.m);
+                    if (s_uniform[s_child[j]] + bq < res.a * sq.sum * exp2_fast(x * c)) {
                         go = s_child[j];
                         break;
                     }

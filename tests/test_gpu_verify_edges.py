@@ -66,3 +66,24 @@ def test_two_equal_logits(vocab, dtype, off):
         tokens = torch.stack([torch.zeros_like(child), child], 1).int()
         _, accepted, nxt, status = greedy(logits, tokens)
         assert torch.equal(nxt.long(), low) and bool((accepted == took).all()) and status == 0
+
+
+@pytest.mark.parametrize("mode", ["certain", "draft", "greedy"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("scale", [1e30, 1e38, 2.0 ** 127])
+def test_lowest_temperatures(scale, dtype, mode):
+    """Products of a logit and the scale that fp32 does not hold; their differences
+    decide.  The 64-bit walk is good up to scales of 1e10, where ln 2 is still
+    seen beside a product.  Differences of these logits are 0 or above 1e-7, so
+    that from there on only the largest logits have any weight and every scale
+    gives the same."""
+    from tests import test_gpu_verify as verify
+
+    verify.S = S
+    for vocab in (60, 5003):
+        c = verify.Case(20, 5, vocab, "tree", mode, dtype, seed=34)
+        c.logits = torch.where(torch.arange(20)[:, None, None] < 10, c.logits, c.logits - 30).to(dtype)
+        c.scale = float(torch.tensor(1e10))
+        want = c.check()
+        assert want[3] == 0 and all(0 <= x < vocab for x in want[2])
+        assert c.run(scale=float(torch.tensor(scale))) == want
