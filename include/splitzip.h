@@ -568,11 +568,12 @@ size_t sz_cache_attend_tree_workspace_size(size_t batch, size_t nodes, size_t q_
  *               SZ_ERR_TIMEOUT as for sz_cache_attend: rows that lack tokens
  *               are NaN
  *  d_ws         256-byte aligned workspace, contents irrelevant
- * Queries enter exactly, but for 2^-37 of a row's largest value; K does where a
- * token's scales lie within 2^12 of their largest, and otherwise to 2^-19 of
- * that; V and the weights are rounded to bfloat16.  A node does not see what
- * other nodes hold, infinities and NaN included.  Range: values of V below 2^30,
- * else infinities; a weight, or a weight times V, below 2^-86 loses bits.
+ * Queries enter exactly, but for 2^-27 of a row's largest value (rows whose sizes
+ * lie within 2^12 share a power of two); K does where a token's scales lie within
+ * 2^12 of their largest, and otherwise to 2^-19 of that; V and the weights are
+ * rounded to bfloat16.  A node does not see what other nodes hold, infinities and
+ * NaN included.  Range: values of V below 2^30, else infinities; a weight, or a
+ * weight times V, below 2^-86 loses bits.
  * Results do not depend on the timing of blocks.  Asynchronous. */
 sz_status sz_cache_attend_tree(const void* d_q, int64_t q_seq_stride, int64_t q_node_stride, int64_t q_head_stride,
                                size_t batch, size_t nodes, size_t q_heads, const void* d_pool, size_t pool_pages,

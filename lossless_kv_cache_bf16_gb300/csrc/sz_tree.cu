@@ -71,7 +71,9 @@ constexpr float kNone = -FLT_MAX;  // a row's reference before any
 // as rarely as fp32 allows with sums over values up to 2^30.  What is lost below
 // has less than 2^-86 of the largest weight, or of 1 where it is a weight times
 // a value.  Rows whose references lie within 20 share one (20 to 40 above their
-// largest logits), and rows whose queries' sizes lie within 2^12 a factor.
+// largest logits), and rows whose queries' sizes lie within 2^12 a factor: the
+// smallest of them has 2^2 or more as its largest fp16 value, whose steps end at
+// 2^-24.
 constexpr float kAbove = 40.f, kHigh = 80.f, kShare = 20.f;
 constexpr int kShareExp = 12;
 constexpr int kMinExp = -112;      // of a power of two that is taken out

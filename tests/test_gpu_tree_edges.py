@@ -96,3 +96,26 @@ def test_rows_of_a_wide_sequence_that_cannot_be_served():
                            lse=lse, status=status)
     assert status.item() == S.SZ_ERR_INVALID_ARG
     assert all(bool((out[0, j] == 0).all()) for j in range(nodes)) and bool((lse == -float("inf")).all())
+
+
+@pytest.mark.parametrize("nodes,group", [(2, 1), (8, 4), (16, 4)])
+def test_rows_that_share_a_power_of_two(nodes, group):
+    """Every other row 2^-12 of its neighbours, its logits from a channel 2^-26 of
+    its largest: they are good to 2^-27 of a row's largest value in each channel."""
+    c = tree.Case([100], 1, group, 64, 16, nodes, seed=35)
+    c.scale = 0.125
+    k = torch.zeros(100 + nodes, 1, 64)
+    k[:, 0, 1] = 2.0 ** 38 * (1 + torch.arange(100 + nodes) % 7)
+    c.write(k.to(torch.bfloat16), R.normal_bf16(R.gen(9), 100 + nodes, 1, 64), c.slots(0, 100 + nodes))
+    c.q[:] = 0
+    c.q[:, ::2, :, 0] = 1.0
+    c.q[:, 1::2, :, 0] = 2.0 ** -12
+    small = torch.arange(nodes * group).view(nodes, group)[1::2] % 16
+    c.q[0, 1::2, :, 1] = (2.0 ** -38 * (0.25 + small / 8)).to(torch.bfloat16)
+    out, lse = c.run()
+    held, v, scales = T.values(c.pool, c.slots(0, 100 + nodes), 16, 1, 64)
+    assert bool((held[:, 0, 0] == 0).all()) and bool((held[:, 0, 1] >= 2.0 ** 37).all())  # the scales are rounded
+    _, _, want, err = T.attend(c.q[0].cuda(), held, v, scales, c.sees(0).cuda(), c.scale)
+    shared = 2.0 ** -27 * c.q[0].cuda().double().abs().amax(-1) * float(held.abs().sum(-1).max()) * c.scale
+    off = (lse[0].double() - want).abs()
+    assert bool((off <= err + shared + 2.0 ** -18 * (1 + want.abs())).all())
