@@ -178,10 +178,12 @@ class DecodeCache:
         position that its depth gives it; returns the attention [batch, nodes,
         q heads, D] of every node over the context, the nodes above it and
         itself.  counts (int32 [batch]): nodes of each sequence, if not all; the
-        others' results are left as they are, or undefined without out.  The
-        nodes lie behind the context until accept() takes some of them; another
-        draft, step or prompt drops them.  No weights are added up, so that a
-        cache with a budget refuses."""
+        others' results are left as they are, or undefined without out.  With
+        them the cache need only have room for the nodes that are there: a full
+        sequence takes part with none, and one whose nodes do not fit gets rows
+        of zero and is reported by check().  The nodes lie behind the context
+        until accept() takes some of them; another draft, step or prompt drops
+        them.  No weights are added up, so that a cache with a budget refuses."""
         hq, hk, d = self.q_heads, self.kv_heads, self.head_dim
         if self.budget is not None:
             raise ValueError("a cache with a budget takes no drafts: their steps add up no weights")
@@ -191,7 +193,8 @@ class DecodeCache:
         for name, t, shape in (("parents", parents, (self.batch, nodes)), ("counts", counts, (self.batch,))):
             if t is not None and (t.shape != shape or t.dtype != torch.int32 or t.device != self.device):
                 raise ValueError(f"{name} must be int32 of shape {list(shape)} on the cache's GPU")
-        if max(self.held) + nodes > self.capacity:
+        over = max(self.held) + nodes > self.capacity
+        if over and counts is None:
             raise ValueError("the cache is full")
         shape = (self.batch, nodes, hq, d)
         if out is None:
@@ -211,8 +214,13 @@ class DecodeCache:
             self.tree_ws = torch.empty(need, dtype=torch.uint8, device=self.device)
         mask, depth = tree_masks(parents)
         positions = (self.next_pos[:, None] + depth).flatten()
-        at = self.lens.long()[:, None] + torch.arange(nodes, device=self.device)
-        slots = (self.table.gather(1, at // self.page).long() * self.page + at % self.page).flatten()
+        own = torch.arange(nodes, device=self.device)
+        at = self.lens.long()[:, None] + own
+        if over:  # a node that is not there, or not within the cache, has no slot
+            left_out = (at >= self.capacity) | (own >= counts[:, None])
+            at = at.clamp_max(self.capacity - 1)
+        slots = self.table.gather(1, at // self.page).long() * self.page + at % self.page
+        slots = (slots.masked_fill(left_out, -1) if over else slots).flatten()
         S.sz_qk_norm_rope(q, k, q_weight, k_weight, eps, inv_freq, positions, q, k)
         S.sz_cache_append(k, v, slots, self.pool, self.page, positions=positions, weight=self.weight, pos=self.pos)
         self.drafted = nodes
