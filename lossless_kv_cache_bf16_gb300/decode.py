@@ -111,11 +111,11 @@ class DecodeCache:
         n, at = k.shape[0], self.held[sequence]
         if at + n > self.capacity:
             raise ValueError(f"{at + n} tokens do not fit in {self.capacity}")
-        self.drafted = 0
         slot = torch.arange(at, at + n, device=self.device)
         slots = self.table[sequence].long()[slot // self.page] * self.page + slot % self.page
         positions = self.next_pos[sequence] + torch.arange(n, dtype=torch.int32, device=self.device)
         S.sz_cache_append(k, v, slots, self.pool, self.page, positions=positions, weight=self.weight, pos=self.pos)
+        self.drafted = 0
         self.lens[sequence] += n
         self.next_pos[sequence] += n
         self.held[sequence] += n
@@ -154,11 +154,11 @@ class DecodeCache:
             out = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
         else:  # before the token joins the cache: the attention's own refusal would come after it
             S.check_output(out, shape, q)
-        self.drafted = 0
         S.sz_qk_norm_rope(q, k, q_weight, k_weight, eps, inv_freq, self.next_pos, q, k)
         at = self.lens.long()
         slots = self.table.gather(1, (at // self.page)[:, None])[:, 0].long() * self.page + at % self.page
         S.sz_cache_append(k, v, slots, self.pool, self.page, positions=self.next_pos, weight=self.weight, pos=self.pos)
+        self.drafted = 0
         self.lens += 1
         self.next_pos += 1
         self.held = [n + 1 for n in self.held]

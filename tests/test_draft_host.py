@@ -49,3 +49,27 @@ def test_counts_do_not_matter_to_slots_where_there_is_room(cache):
     for counts in (None, i32([3, 1])):
         cache.draft(bf16(2, 3, 8, 64), i32([[0, 0, 1], [0, 0, 0]]), None, None, torch.ones(32), counts=counts)
     assert cache.slots == [[50, 51, 52, 64, 65, 66]] * 2
+
+
+def test_a_refused_prompt_or_step_leaves_the_draft(cache, monkeypatch):
+    from lossless_kv_cache_bf16_gb300 import decode
+
+    freq = torch.ones(32)
+    cache.extend(0, bf16(5, 2, 64), bf16(5, 2, 64))
+    cache.draft(bf16(2, 3, 8, 64), i32([[0, 0, 1], [0, 0, 0]]), None, None, freq)
+
+    def refuse(*_, **__):
+        raise ValueError("refused")
+
+    with monkeypatch.context() as m:
+        m.setattr(decode.S, "sz_cache_append", refuse)
+        for call in (lambda: cache.extend(1, bf16(2, 2, 64).float(), bf16(2, 2, 64).float()),
+                     lambda: cache.step(bf16(2, 8, 64), None, None, freq)):
+            with pytest.raises(ValueError, match="refused"):
+                call()
+        m.setattr(decode.S, "sz_qk_norm_rope", refuse)
+        with pytest.raises(ValueError, match="refused"):
+            cache.step(bf16(2, 8, 64), None, None, freq)
+    assert cache.held == [5, 0] == cache.lens.tolist() == cache.next_pos.tolist()
+    cache.accept(i32([[0, 1, -1], [0, -1, -1]]), i32([2, 1]))
+    assert cache.held == [7, 1]
