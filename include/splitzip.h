@@ -560,6 +560,7 @@ size_t sz_cache_attend_tree_workspace_size(size_t batch, size_t nodes, size_t q_
  *               attends to node j, its own bit included.  Bits from the
  *               sequence's count on do not matter.  A node without a context
  *               and without a bit gives zero rows (log-sum -infinity)
+ *  scale        of size up to 2^127
  *  d_lse        nullable: float [batch][nodes][q_heads], as for sz_cache_attend
  *  d_status     nullable; SZ_OK, SZ_ERR_INVALID_ARG (also for a negative
  *               length or one with which the nodes do not fit into the table's
@@ -572,8 +573,8 @@ size_t sz_cache_attend_tree_workspace_size(size_t batch, size_t nodes, size_t q_
  * lie within 2^12 share a power of two); K does where a token's scales lie within
  * 2^12 of their largest, and otherwise to 2^-19 of that; V and the weights are
  * rounded to bfloat16.  A node does not see what other nodes hold, infinities and
- * NaN included.  Range: values of V below 2^30, else infinities; a weight, or a
- * weight times V, below 2^-86 loses bits.
+ * NaN included.  Range: logits within fp32, else NaN; values of V below 2^30,
+ * else infinities; a weight, or a weight times V, below 2^-86 loses bits.
  * Results do not depend on the timing of blocks.  Asynchronous. */
 sz_status sz_cache_attend_tree(const void* d_q, int64_t q_seq_stride, int64_t q_node_stride, int64_t q_head_stride,
                                size_t batch, size_t nodes, size_t q_heads, const void* d_pool, size_t pool_pages,

@@ -220,7 +220,7 @@ sz_status attend_tree(const char* name, uint32_t stalled_block, const void* d_q,
     if (!pool_for(d_pool, pool_pages, kv_heads, head_dim, page_tokens, &p.pool)) return SZ_ERR_INVALID_ARG;
     if (batch > 0 && !table_ok(d_table, table_width, page_tokens)) return SZ_ERR_INVALID_ARG;
     const uint64_t max_tokens = batch > 0 ? (uint64_t)table_width * page_tokens : page_tokens;
-    if (!tree_sizes_ok(batch, nodes, q_heads, kv_heads, head_dim, max_tokens) || !std::isfinite(scale)) return SZ_ERR_INVALID_ARG;
+    if (!tree_sizes_ok(batch, nodes, q_heads, kv_heads, head_dim, max_tokens) || !(std::fabs(scale) <= 0x1p127f)) return SZ_ERR_INVALID_ARG;
     if ((d_status && !aligned(d_status, 4)) || (d_lse && !aligned(d_lse, 4)) || (d_counts && !aligned(d_counts, 4)))
         return SZ_ERR_INVALID_ARG;
     if (batch == 0) return clear_status(d_status, stream);

@@ -73,3 +73,13 @@ def test_a_refused_prompt_or_step_leaves_the_draft(cache, monkeypatch):
     assert cache.held == [5, 0] == cache.lens.tolist() == cache.next_pos.tolist()
     cache.accept(i32([[0, 1, -1], [0, -1, -1]]), i32([2, 1]))
     assert cache.held == [7, 1]
+
+
+@pytest.mark.parametrize("scale", [3e38, -3e38, 2.0 ** 127 * (1 + 2.0 ** -23)])
+def test_scales_beyond_what_a_product_with_log2_e_holds_are_refused(scale):
+    from lossless_kv_cache_bf16_gb300 import splitzip as S
+    from tests.test_cache_host import call
+    from tests.test_tree_host import TREE
+
+    assert call(S.LIB, "sz_cache_attend_tree", TREE, scale=scale, ws_bytes=0) == S.SZ_ERR_INVALID_ARG
+    assert call(S.LIB, "sz_cache_attend_tree", TREE, scale=-2.0 ** 127, ws_bytes=0) != S.SZ_ERR_INVALID_ARG
