@@ -77,6 +77,7 @@ constexpr float kNone = -FLT_MAX;  // a row's reference before any
 constexpr float kAbove = 40.f, kHigh = 80.f, kShare = 20.f;
 constexpr int kShareExp = 12;
 constexpr int kMinExp = -112;      // of a power of two that is taken out
+constexpr uint32_t kMostScale = 0x7E117E11u;  // the largest bf16 number whose sevenfold is one, twice
 
 template <int D, int N>
 struct Shape {
@@ -787,16 +788,24 @@ __global__ void __launch_bounds__(Shape<D, N>::kThreads, 1) tree_kernel(const Tr
 #pragma unroll 1
                                 for (uint32_t h = 0; h < 8; h++) {
                                     const uint32_t k = h >> 1, tk = 8 * (k & 1) + 2 * x + (h & 1), cc = c + (k >> 1);
-                                    const uint32_t token = t * kTile + 16 * cc + tk, half = 0xFFFFu << (16 * (h & 1)), inf = half & 0x7F807F80u;
+                                    const uint32_t token = t * kTile + 16 * cc + tk, half = 0xFFFFu << (16 * (h & 1));
+                                    const uint32_t size = half & 0x7FFF7FFFu, inf = half & 0x7F807F80u, most = half & kMostScale;
                                     const uint32_t s0 = k == 0 ? sc[0] : k == 1 ? sc[1] : k == 2 ? sc[2] : sc[3];
-                                    const bool there = tk < s_valid[stage][cc], off = there && token >= s.len && (s0 & inf) == inf;
-                                    // Not finite: seen by some rows only, which get it at the end.
-                                    if (off)
-                                        for (int q = 0; q < SG; q++) atomicOr(&s_nan[seg & 7u][q][i], 1ull << (token - s.len & 63u));
+                                    const bool there = tk < s_valid[stage][cc], off = there && token >= s.len && (s0 & size) > most;
                                     if (!there || off) {
+                                        uint32_t now = s0 & ~half;
+                                        if (off) {
+                                            // Not finite: seen by some rows only, which get it at the end.
+                                            // Finite, but not its sevenfold: the next smaller scale, as an
+                                            // infinity would reach rows with a weight of 0.
+                                            if ((s0 & size) < inf)
+                                                now = (s0 & ~size) | most;
+                                            else
+                                                for (int q = 0; q < SG; q++) atomicOr(&s_nan[seg & 7u][q][i], 1ull << (token - s.len & 63u));
+                                        }
 #pragma unroll
                                         for (uint32_t y = 0; y < 4; y++)
-                                            if (y == k) sc[y] &= ~half;
+                                            if (y == k) sc[y] = now;
                                     }
                                 }
                             }

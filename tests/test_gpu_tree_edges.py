@@ -119,3 +119,23 @@ def test_rows_that_share_a_power_of_two(nodes, group):
     shared = 2.0 ** -27 * c.q[0].cuda().double().abs().amax(-1) * float(held.abs().sum(-1).max()) * c.scale
     off = (lse[0].double() - want).abs()
     assert bool((off <= err + shared + 2.0 ** -18 * (1 + want.abs())).all())
+
+
+@pytest.mark.parametrize("bad", [0x7F7F, -0x0081, 0x7F70])
+@pytest.mark.parametrize("dim,nodes,group", [(64, 4, 4), (128, 6, 4), (128, 16, 8)])
+def test_a_node_of_the_largest_values(dim, nodes, group, bad):
+    """V of the largest bf16 numbers, which the cache holds as more than that: rows
+    that do not attend to the node are as if it held zero, and no row is NaN."""
+    big = float(torch.tensor([bad], dtype=torch.int16).view(torch.bfloat16)[0])
+    c = tree.Case([30, 0, 125, 127], 2, group, dim, 16, nodes, seed=36)
+    k, v = R.normal_bf16(R.gen(7), 1, 2, dim), torch.zeros(1, 2, dim, dtype=torch.bfloat16)
+    outs = []
+    for value in (0.0, big):
+        v[0, :, 5], v[0, :, 37] = value, -value
+        for b, n in enumerate(c.lens):
+            c.write(k, v, c.slots(b, n + nodes)[n + 2:n + 3])
+        outs.append(c.run())
+    sees = (c.mask >> 2 & 1).bool()
+    assert bool(sees.any()) and not bool(sees.all())
+    assert not bool(torch.isnan(outs[1][0]).any()) and torch.equal(outs[0][1], outs[1][1])
+    assert torch.equal(outs[0][0][~sees], outs[1][0][~sees])
