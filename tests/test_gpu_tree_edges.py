@@ -139,3 +139,22 @@ def test_a_node_of_the_largest_values(dim, nodes, group, bad):
     assert bool(sees.any()) and not bool(sees.all())
     assert not bool(torch.isnan(outs[1][0]).any()) and torch.equal(outs[0][1], outs[1][1])
     assert torch.equal(outs[0][0][~sees], outs[1][0][~sees])
+
+
+@pytest.mark.parametrize("lens,counts", [([20000, 300, 9000], [8, 16, 3]), ([40] * 400, [1, 16, 8, 12] * 100)])
+def test_a_wait_that_gives_up_beside_few_rows(lens, counts):
+    """As in test_gpu_tree.py, with items that have no rows for some warps."""
+    c = tree.Case(lens, 1, 4, 128, 64, 16, seed=37, counts=counts)
+    want = c.run()
+    S, (b, n, hq, d) = tree.S, c.q.shape
+    ws = torch.empty(S.sz_cache_attend_tree_workspace_size(b, n, hq, 1, d, c.table.shape[1] * 64), dtype=torch.uint8, device="cuda")
+    out, lse = torch.full_like(want[0], 7.0), torch.full_like(want[1], 7.0)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    S.sz_debug_attend_tree_stalled(c.q.cuda(), c.pool, 1, 64, c.table.cuda(), i32(lens), c.mask.cuda(), c.scale, out, ws, counts=i32(counts),
+                                   lse=lse, status=status)
+    assert status.item() == S.SZ_ERR_TIMEOUT
+    lost = torch.isnan(out).all(-1)
+    assert bool(lost[0, :counts[0]].all()) and bool((torch.isnan(lse) == lost).all())
+    assert torch.equal(out[~lost], want[0][~lost])
+    assert all(torch.equal(x, y) for x, y in zip(c.run(), want))
