@@ -8,7 +8,7 @@
 // first one.  Bound by latency: three dependent loads (path, table, token) and a
 // few kilobytes a block.  Measured (GB300): 256 sequences of 64 nodes, 8 heads of
 // 64 channels: 7.9 us, 7.5 with half the threads and two rounds, 7.1 with a
-// quarter; 64 sequences of 32 nodes: 3.1, and 4.0 with a quarter.
+// quarter; 64 sequences of 32 nodes: 2.9, and 4.0 with a quarter.
 #include <type_traits>
 
 #include "sz_cache.cuh"

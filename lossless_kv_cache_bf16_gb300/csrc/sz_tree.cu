@@ -42,12 +42,14 @@
 // Measured (GB300, 128 channels): 16 sequences of 32,768 tokens, 8 nodes, 7 query
 // heads per kv head, 4 kv heads: 128 us, 304 MB at 2.4 TB/s.  4 sequences of
 // 32,768, 64 nodes: 208 us, 120 GFLOP at 579 TFLOP/s.  16 ragged sequences up to
-// 8,192, 32 nodes: 44 us.  A tile of 128 tokens and 64 rows is 5,700 warp
-// instructions, a quarter each for K, V, softmax, and waits and addresses, and
-// takes 1,900 clocks: the schedulers issue in two of three, the ALU pipe is busy
-// for 60%, the matrix unit for 23%, and memory gives a third of what it could.  So
-// the unpacking of codes bounds it at every number of rows: it is done once for
-// 64 rows.
+// 8,192, 32 nodes: 44 us.  A tile of 128 tokens and 64 rows is 5,800 warp
+// instructions (1,450 issue slots of a scheduler), a quarter each for K, V, softmax,
+// and waits and addresses, and takes 1,900 clocks.  That is the way of a softmax
+// group through it, one thing after the other: 370 clocks until the logits are
+// there, 540 to load them, 715 for the weights, 300 for the fence and the vote.
+// K's and V's warps idle for half of that; the schedulers issue in two of three
+// cycles, the ALU pipe is busy for 58%, the matrix unit for 25%, and memory gives a
+// third of what it could.
 #include <cfloat>
 
 #include "sz_cache.cuh"
@@ -58,10 +60,11 @@ namespace sz {
 namespace {
 
 constexpr uint32_t kTile = 128;  // tokens of a tile
-// Tiles that an item's start and end cost.  Measured with 4 / 5 / 6 / 8 / 10:
-// ragged batch of 16, 32 nodes: 48.3 / 46.6 / 43.6 / 46.7 / 47.9 us; 4 sequences of
-// 2,048, chains of 4: 16.7 / 17.0 / 17.2 / 17.6 / 17.0; 16 of 32,768, 8 nodes: 128.7 /
-// 129.0 / 128.9 / 130.9 / 130.8.
+// Tiles that an item's start and end count for in the split.  Measured with 4 / 5 /
+// 6 / 8 / 10: a ragged batch of 16, 32 nodes: 48.3 / 46.6 / 43.6 / 46.7 / 47.9 us; 4
+// sequences of 2,048, chains of 4: 16.7 / 17.0 / 17.2 / 17.6 / 17.0; 16 of 32,768, 8
+// nodes: 128.7 / 129.0 / 128.9 / 130.9 / 130.8.  The dip of the first is where the
+// cuts of that one list fall; by the others anything up to 6 will do.
 constexpr uint32_t kItemCost = 6;
 constexpr uint32_t kJoinThreads = 512;
 constexpr float kNegInf = -__builtin_huge_valf();

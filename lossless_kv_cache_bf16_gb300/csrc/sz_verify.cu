@@ -4,14 +4,15 @@
 // One cluster of blocks per sequence walks down its tree: only the rows of
 // nodes that the walk comes through are read.  At a node one pass over the row
 // gives the sum of exponentials of all but the children's tokens, which are
-// looked up one by one.  So a node costs one reading of its row however many
-// children it has, and nothing is taken out of a sum again: with W the sum over
-// the other tokens and w_j the children's, child j is accepted if
+// looked up one by one.  So without draft logits a node costs one reading of its
+// row however many children it has, and nothing is taken out of a sum again: with W
+// the sum over the other tokens and w_j the children's, child j is accepted if
 // u_j (W + sum of w_i, i >= j) < w_j.  Where none is, a second pass over the
 // row, which is in L1 by then, draws among the other tokens; noise is read there
 // alone.  With draft logits the residual is max(a p - b q, 0), a and b two
 // numbers that a rejection changes: max(r / s - q, 0) with s the sum of r gives
-// a / s and (b + s) / s times s; a further pass over both rows gives each sum.
+// a / s and (b + s) / s times s; a further pass over both rows gives each sum, one
+// for every rejected child but the last.
 //
 // Sums.  exp(scale (l - m)) with m a largest logit, so that the difference is
 // good to its own size.  A thread has its own m; maxima and sums are joined in
