@@ -111,6 +111,9 @@ struct Shape {
     static constexpr uint32_t kV = D + 4 * 64 + 3 * N <= 512 ? 4 : 2;
     static constexpr uint32_t kKCol = 0, kVCol = D, kSCol = D + 64 * kV, kOCol = kSCol + 2 * N;
     static_assert(kOCol + N <= 512 && kStages >= 3, "tensor memory, ring");
+    // The two sets of K's and of V's warps take every other tile, and each has to
+    // see every phase of its stages and buffers: a parity tells neighbours only.
+    static_assert(kStages % 2 == 0 && kV % 2 == 0, "stages of a set");
 };
 
 struct Bars {
