@@ -659,7 +659,7 @@ sz_status sz_verify_tree(const void* d_logits, int logits_f32, int64_t seq_strid
  *  d_weight,    nullable: the tables beside the pool
  *  d_pos
  *  d_new_lens   int32 per sequence: length + accepted; refused where it shares
- *               memory with d_lens or d_accepted.  A sequence whose length,
+ *               memory with d_lens, d_path or d_accepted.  A sequence whose length,
  *               path or accepted number is not as above, whose accepted nodes
  *               do not lie within the table's width, or one of whose moves
  *               meets a page id outside the pool keeps its length (0 for one outside the table)
